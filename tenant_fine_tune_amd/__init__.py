@@ -23,7 +23,8 @@ __all__ = ["lib", "lib_path", "BitDeltaError", "compress", "reconstruct", "linea
            "linear_grouped_noalloc", "similarity_delta", "monosoup", "MONOSOUP_SKETCH", "DeltaCache", "LOADER",
            "BD_OK", "BD_EINVAL", "BD_ESHAPE", "BD_EALIGN", "BD_EWORKSPACE", "BD_EDEVICE", "BD_EBUSY",
            "BD_CACHE_HIT", "BD_CACHE_MISS", "BD_CACHE_JOINED",
-           "BD_BF16", "BD_F32", "BD_ALPHA_ROW", "BD_ALPHA_MATRIX", "EXPORTS"]
+           "BD_BF16", "BD_F32", "BD_ALPHA_ROW", "BD_ALPHA_MATRIX", "EXPORTS",
+           "block_norm", "kv_append", "attention", "PagedKV", "PagedBatch"]
 
 BD_OK, BD_EINVAL, BD_ESHAPE, BD_EALIGN, BD_EWORKSPACE, BD_EDEVICE, BD_EBUSY = range(7)
 BD_CACHE_HIT, BD_CACHE_MISS, BD_CACHE_JOINED = 0, 1, 2
@@ -63,6 +64,12 @@ EXPORTS = {
     "bitdelta_probe_read": (_INT, [_P, _I64, _P, _P]),
     "bitdelta_probe_mfma": (_INT, [_I32, _I32, ctypes.c_float, ctypes.c_float, _P, _P]),
     "bitdelta_probe_lds": (_INT, [_I32, _I32, _I32, _I32, _P, _I64, _P, _P, _P]),
+    # include/bitdelta_decoder.h
+    "bitdelta_block_norm": (_INT, [_P, _I64, _INT, _P, _I64, _P, _I64, _INT, ctypes.c_float, _P, _P, _INT, _P, _I32,
+                                   _I64, _I64, ctypes.c_float, _P, _I64, _P, _P]),
+    "bitdelta_kv_append": (_INT, [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _I32, _INT, _P, _P, _P, _P]),
+    "bitdelta_attention_workspace": (_SZ, [_I32, _P, _P]),
+    "bitdelta_attention": (_INT, [_P, _I64, _I32, ctypes.c_float, _P, _P, _P, _P, _SZ, _P]),
     # include/bitdelta_cache.h
     "bitdelta_cache_create": (_INT, [_I32, _I32, _I32, _I64, _P, _SZ, _P, _P, _P]),
     "bitdelta_cache_destroy": (None, [_P]),
@@ -463,3 +470,16 @@ class DeltaCache:
 
     def __del__(self):
         self.close()
+
+
+_DECODER = ("block_norm", "kv_append", "attention", "PagedKV", "PagedBatch")
+
+
+def __getattr__(name):
+    # the operators between the linears; their module needs torch, which the
+    # package itself imports only when a call does
+    if name in _DECODER:
+        from . import decoder
+
+        return globals().setdefault(name, getattr(decoder, name))
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -13,6 +13,7 @@
 
 #include "../../include/bitdelta.h"
 #include "bd_launch.h"
+#include "decoder_launch.h"
 
 namespace {
 
@@ -497,6 +498,223 @@ bd_status bitdelta_probe_lds(int32_t blocks, int32_t iters, int32_t mode, int32_
     BD_ALIGNED(cycles, 8);
     return device(bd::launch_probe_lds(blocks, iters, mode, stride, src, src_bytes, sink, cycles, (hipStream_t)stream),
                   "bitdelta_probe_lds");
+}
+
+// ---------------------------------------------- between the linears of a layer
+
+namespace {
+
+bd_status check_cache(const bd_kv_cache *cache)
+{
+    BD_NONNULL(cache);
+    const bd_kv_cache &c = *cache;
+    if (c.dtype != BD_KV_BF16 && c.dtype != BD_KV_E4M3)
+        return fail(BD_EINVAL, "cache dtype must be BD_KV_BF16 (0) or BD_KV_E4M3 (1), got %d", c.dtype);
+    if (c.n_pages < 1 || c.n_kv_heads < 1 || c.n_kv_heads > 1024)
+        return fail(BD_ESHAPE, "cache needs n_pages >= 1 and n_kv_heads in [1, 1024] (got %d, %d)", c.n_pages,
+                    c.n_kv_heads);
+    if (c.page_size < 1 || c.page_size > 1024 || (c.page_size & (c.page_size - 1)) != 0)
+        return fail(BD_ESHAPE, "page_size must be a power of two in [1, 1024] (got %d)", c.page_size);
+    if (c.head_dim != 64 && c.head_dim != 128)
+        return fail(BD_ESHAPE, "head_dim must be 64 or 128 (got %d)", c.head_dim);
+    if (c.dtype == BD_KV_BF16 && (c.k_scale || c.v_scale))
+        return fail(BD_EINVAL, "a bf16 cache takes no k_scale or v_scale");
+    BD_NONNULL(c.k);
+    BD_NONNULL(c.v);
+    BD_ALIGNED(c.k, 16);
+    BD_ALIGNED(c.v, 16);
+    BD_ALIGNED(c.k_scale, 4);
+    BD_ALIGNED(c.v_scale, 4);
+    return BD_OK;
+}
+
+bd_status check_batch(const bd_batch *batch)
+{
+    BD_NONNULL(batch);
+    const bd_batch &b = *batch;
+    if (b.n_tokens < 0 || b.n_tokens > kMaxGrid)
+        return fail(BD_ESHAPE, "n_tokens must be in [0, 2^31) (got %lld)", (long long)b.n_tokens);
+    if (b.n_seqs < 0 || b.n_seqs > BD_MAX_SEQS || b.n_groups < 0 || b.n_groups > BD_MAX_SEQS)
+        return fail(BD_ESHAPE, "n_seqs and n_groups must be in [0, %d] (got %d, %d)", BD_MAX_SEQS, b.n_seqs,
+                    b.n_groups);
+    if (b.max_new < 0)
+        return fail(BD_ESHAPE, "max_new must not be negative (got %d)", b.max_new);
+    if (b.n_seqs > 0) {
+        if (b.max_pages < 1)
+            return fail(BD_ESHAPE, "max_pages must be positive (got %d)", b.max_pages);
+        BD_NONNULL(b.q_start);
+        BD_NONNULL(b.kv_len);
+        BD_NONNULL(b.page_table);
+        BD_ALIGNED(b.q_start, 4);
+        BD_ALIGNED(b.kv_len, 4);
+        BD_ALIGNED(b.page_table, 4);
+    }
+    if (b.n_groups > 0) {
+        if (b.max_prefix_pages < 1)
+            return fail(BD_ESHAPE, "max_prefix_pages must be positive (got %d)", b.max_prefix_pages);
+        BD_NONNULL(b.group_start);
+        BD_NONNULL(b.prefix_len);
+        BD_NONNULL(b.prefix_table);
+        BD_ALIGNED(b.group_start, 4);
+        BD_ALIGNED(b.prefix_len, 4);
+        BD_ALIGNED(b.prefix_table, 4);
+    }
+    return BD_OK;
+}
+
+bd_status check_rows(const char *name, int64_t stride, int64_t width, int64_t multiple)
+{
+    if (stride < width || stride % multiple != 0 || stride > (int64_t)1 << 40)
+        return fail(BD_ESHAPE, "%s row stride must be a multiple of %lld and at least %lld (got %lld)", name,
+                    (long long)multiple, (long long)width, (long long)stride);
+    return BD_OK;
+}
+
+bd_status check_heads(int32_t n_heads, const bd_kv_cache &c)
+{
+    if (n_heads < 1 || n_heads > 1024 || n_heads % c.n_kv_heads != 0)
+        return fail(BD_ESHAPE, "n_heads must be a multiple of n_kv_heads = %d in [1, 1024] (got %d)", c.n_kv_heads,
+                    n_heads);
+    return BD_OK;
+}
+
+}  // namespace
+
+bd_status bitdelta_block_norm(const void *residual, int64_t residual_stride, int residual_dtype, const bd_bf16 *block,
+                              int64_t block_stride, const bd_bf16 *gate, int64_t gate_stride, int gate_act,
+                              float scale, const void *post_weight, const void *pre_weight, int weight_dtype,
+                              const int32_t *variant_ids, int32_t n_variants, int64_t m, int64_t d, float eps,
+                              void *residual_out, int64_t residual_out_stride, bd_bf16 *x, void *stream)
+{
+    if (residual_dtype != BD_BF16 && residual_dtype != BD_F32)
+        return fail(BD_EINVAL, "residual_dtype must be BD_BF16 (0) or BD_F32 (1), got %d", residual_dtype);
+    if (weight_dtype != BD_BF16 && weight_dtype != BD_F32)
+        return fail(BD_EINVAL, "weight_dtype must be BD_BF16 (0) or BD_F32 (1), got %d", weight_dtype);
+    if (gate_act != BD_GATE_NONE && gate_act != BD_GATE_SIGMOID && gate_act != BD_GATE_SILU)
+        return fail(BD_EINVAL, "gate_act must be BD_GATE_NONE, _SIGMOID or _SILU (0..2), got %d", gate_act);
+    if (n_variants < 1)
+        return fail(BD_EINVAL, "n_variants must be positive (got %d)", n_variants);
+    if (!(eps >= 0.0f))
+        return fail(BD_EINVAL, "eps must not be negative or NaN");
+    if (m < 0 || m > kMaxGrid)
+        return fail(BD_ESHAPE, "m must be in [0, 2^31) (got %lld)", (long long)m);
+    if (d < 1 || d > BD_NORM_MAX_WIDTH)
+        return fail(BD_ESHAPE, "d must be in [1, %d] (got %lld)", BD_NORM_MAX_WIDTH, (long long)d);
+    if (m == 0)   // an empty tensor has no address
+        return BD_OK;
+    if (!block && (post_weight || gate))
+        return fail(BD_EINVAL, "post_weight and gate need a block");
+    if (!pre_weight && !residual_out)
+        return fail(BD_EINVAL, "block_norm has no output: give pre_weight or residual_out");
+    BD_NONNULL(residual);
+    BD_TRY(check_rows("residual", residual_stride, d, 1));
+    const size_t re = residual_dtype == BD_F32 ? 4 : 2, we = weight_dtype == BD_F32 ? 4 : 2;
+    BD_ALIGNED(residual, re);
+    if (block) {
+        BD_TRY(check_rows("block", block_stride, d, 1));
+        BD_ALIGNED(block, 2);
+    }
+    if (gate) {
+        BD_TRY(check_rows("gate", gate_stride, d, 1));
+        BD_ALIGNED(gate, 2);
+    }
+    if (residual_out) {
+        BD_TRY(check_rows("residual_out", residual_out_stride, d, 1));
+        BD_ALIGNED(residual_out, re);
+        if (residual_out == residual && residual_out_stride != residual_stride)
+            return fail(BD_EINVAL, "residual_out over residual needs the same row stride");
+    }
+    if (pre_weight) {
+        BD_NONNULL(x);
+        BD_ALIGNED(x, 2);
+    }
+    BD_ALIGNED(post_weight, we);
+    BD_ALIGNED(pre_weight, we);
+    BD_ALIGNED(variant_ids, 4);
+    bd::NormArgs a;
+    a.residual = residual, a.block = block, a.gate = gate, a.post_weight = post_weight, a.pre_weight = pre_weight;
+    a.ids = variant_ids, a.residual_out = residual_out, a.x = x;
+    a.residual_stride = residual_stride, a.block_stride = block_stride, a.gate_stride = gate_stride;
+    a.out_stride = residual_out_stride, a.m = m;
+    a.n_variants = n_variants, a.d = (int32_t)d, a.gate_act = gate_act, a.scale = scale, a.eps = eps;
+    a.residual_f32 = residual_dtype == BD_F32, a.weight_f32 = weight_dtype == BD_F32;
+    return device(bd::launch_block_norm(a, (hipStream_t)stream), "bitdelta_block_norm");
+}
+
+bd_status bitdelta_kv_append(const bd_bf16 *q, int64_t q_stride, const bd_bf16 *k, int64_t k_stride, const bd_bf16 *v,
+                             int64_t v_stride, int32_t n_heads, const double *inv_freq, int32_t rotary,
+                             int interleaved, const bd_kv_cache *cache, const bd_batch *batch, bd_bf16 *q_out,
+                             void *stream)
+{
+    BD_TRY(check_cache(cache));
+    BD_TRY(check_batch(batch));
+    if (interleaved != 0 && interleaved != 1)
+        return fail(BD_EINVAL, "interleaved must be 0 or 1 (got %d)", interleaved);
+    if (rotary < 0 || rotary > cache->head_dim || rotary % 16 != 0)
+        return fail(BD_ESHAPE, "rotary must be a multiple of 16 in [0, head_dim] (got %d)", rotary);
+    if (n_heads != 0)
+        BD_TRY(check_heads(n_heads, *cache));
+    else if (q || q_out)
+        return fail(BD_EINVAL, "q and q_out must be NULL where n_heads is 0");
+    if (batch->n_tokens == 0)
+        return BD_OK;
+    BD_NONNULL(k);
+    BD_NONNULL(v);
+    BD_ALIGNED(k, 16);
+    BD_ALIGNED(v, 16);
+    BD_TRY(check_rows("k", k_stride, (int64_t)cache->n_kv_heads * cache->head_dim, 8));
+    BD_TRY(check_rows("v", v_stride, (int64_t)cache->n_kv_heads * cache->head_dim, 8));
+    if (n_heads) {
+        BD_NONNULL(q);
+        BD_NONNULL(q_out);
+        BD_ALIGNED(q, 16);
+        BD_ALIGNED(q_out, 16);
+        BD_TRY(check_rows("q", q_stride, (int64_t)n_heads * cache->head_dim, 8));
+        if (q_out == q && q_stride != (int64_t)n_heads * cache->head_dim)
+            return fail(BD_EINVAL, "q_out over q needs a dense q");
+    }
+    if (rotary) {
+        BD_NONNULL(inv_freq);
+        BD_ALIGNED(inv_freq, 8);
+    }
+    return device(bd::launch_kv_append(q, q_stride, k, k_stride, v, v_stride, n_heads, inv_freq, rotary,
+                                       interleaved != 0, *cache, *batch, q_out, (hipStream_t)stream),
+                  "bitdelta_kv_append");
+}
+
+size_t bitdelta_attention_workspace(int32_t n_heads, const bd_kv_cache *cache, const bd_batch *batch)
+{
+    if (check_cache(cache) != BD_OK || check_batch(batch) != BD_OK || check_heads(n_heads, *cache) != BD_OK)
+        return 0;
+    return bd::attention_workspace_bytes(n_heads, *cache, *batch);
+}
+
+bd_status bitdelta_attention(const bd_bf16 *q, int64_t q_stride, int32_t n_heads, float scale,
+                             const bd_kv_cache *cache, const bd_batch *batch, bd_bf16 *out, void *workspace,
+                             size_t workspace_bytes, void *stream)
+{
+    BD_TRY(check_cache(cache));
+    BD_TRY(check_batch(batch));
+    BD_TRY(check_heads(n_heads, *cache));
+    if (!(scale > 0.0f) || scale > std::numeric_limits<float>::max())
+        return fail(BD_EINVAL, "scale must be positive and finite");
+    if (batch->n_tokens == 0)
+        return BD_OK;
+    BD_NONNULL(q);
+    BD_NONNULL(out);
+    BD_ALIGNED(q, 16);
+    BD_ALIGNED(out, 16);
+    BD_TRY(check_rows("q", q_stride, (int64_t)n_heads * cache->head_dim, 8));
+    const size_t need = bd::attention_workspace_bytes(n_heads, *cache, *batch);
+    if (workspace_bytes < need)
+        return fail(BD_EWORKSPACE, "attention needs %zu workspace bytes, got %zu", need, workspace_bytes);
+    if (need) {
+        BD_NONNULL(workspace);
+        BD_ALIGNED(workspace, 16);
+    }
+    return device(bd::launch_attention(q, q_stride, n_heads, scale, *cache, *batch, out, workspace,
+                                       (hipStream_t)stream),
+                  "bitdelta_attention");
 }
 
 }  // extern "C"
