@@ -53,7 +53,8 @@ BD_API bd_status bitdelta_block_norm(const void *residual, int64_t residual_stri
 
 /* ------------------------------------------------------------- paged cache
  * k and v: [n_pages, n_kv_heads, page_size, head_dim], dense, 16-byte aligned.
- * page_size: a power of two in [1, 1024]; head_dim: 64 or 128.
+ * page_size: a power of two in [1, 1024]; head_dim: 64 or 128; n_kv_heads at
+ * most 1024; n_pages * n_kv_heads * page_size below 2^31.
  * dtype BD_KV_E4M3: a stored number stands for number * scale[head], with
  * k_scale / v_scale fp32 [n_kv_heads] (NULL: 1); BD_KV_BF16 takes no scales. */
 typedef enum { BD_KV_BF16 = 0, BD_KV_E4M3 = 1 } bd_kv_dtype;
@@ -80,12 +81,13 @@ typedef struct {
  * position is prefix_len[g] + its place.  n_groups = 0: no prefixes, the
  * three pointers may be NULL.
  * Bounds kept on the device: starts are clamped to [0, n_tokens], lengths to
- * what the table's columns hold; a place below 0 or a page number outside
+ * what the table's columns hold and to 2^30; a place below 0 or a page number outside
  * [0, n_pages) holds no key (nothing is stored there and attention passes it
  * over).
  * max_new: the largest number of new tokens of one sequence, or 0 where the
  * caller does not know it; a hint for the choice of kernels that no result
- * depends on.  n_seqs, n_groups <= BD_MAX_SEQS. */
+ * depends on.  n_seqs, n_groups <= BD_MAX_SEQS; n_tokens < 2^31, and
+ * n_tokens * n_heads < 2^31 in the calls that take queries. */
 #define BD_MAX_SEQS 4096
 
 typedef struct {

@@ -517,6 +517,9 @@ bd_status check_cache(const bd_kv_cache *cache)
         return fail(BD_ESHAPE, "page_size must be a power of two in [1, 1024] (got %d)", c.page_size);
     if (c.head_dim != 64 && c.head_dim != 128)
         return fail(BD_ESHAPE, "head_dim must be 64 or 128 (got %d)", c.head_dim);
+    // a cell's number is 32 bits wide in the kernels (its address is not)
+    if ((int64_t)c.n_pages * c.n_kv_heads > kMaxGrid / c.page_size)
+        return fail(BD_ESHAPE, "n_pages * n_kv_heads * page_size must be below 2^31");
     if (c.dtype == BD_KV_BF16 && (c.k_scale || c.v_scale))
         return fail(BD_EINVAL, "a bf16 cache takes no k_scale or v_scale");
     BD_NONNULL(c.k);
@@ -570,11 +573,13 @@ bd_status check_rows(const char *name, int64_t stride, int64_t width, int64_t mu
     return BD_OK;
 }
 
-bd_status check_heads(int32_t n_heads, const bd_kv_cache &c)
+bd_status check_heads(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
 {
     if (n_heads < 1 || n_heads > 1024 || n_heads % c.n_kv_heads != 0)
         return fail(BD_ESHAPE, "n_heads must be a multiple of n_kv_heads = %d in [1, 1024] (got %d)", c.n_kv_heads,
                     n_heads);
+    if (b.n_tokens > kMaxGrid / n_heads)
+        return fail(BD_ESHAPE, "n_tokens * n_heads must be below 2^31 (got %lld x %d)", (long long)b.n_tokens, n_heads);
     return BD_OK;
 }
 
@@ -653,7 +658,7 @@ bd_status bitdelta_kv_append(const bd_bf16 *q, int64_t q_stride, const bd_bf16 *
     if (rotary < 0 || rotary > cache->head_dim || rotary % 16 != 0)
         return fail(BD_ESHAPE, "rotary must be a multiple of 16 in [0, head_dim] (got %d)", rotary);
     if (n_heads != 0)
-        BD_TRY(check_heads(n_heads, *cache));
+        BD_TRY(check_heads(n_heads, *cache, *batch));
     else if (q || q_out)
         return fail(BD_EINVAL, "q and q_out must be NULL where n_heads is 0");
     if (batch->n_tokens == 0)
@@ -684,7 +689,7 @@ bd_status bitdelta_kv_append(const bd_bf16 *q, int64_t q_stride, const bd_bf16 *
 
 size_t bitdelta_attention_workspace(int32_t n_heads, const bd_kv_cache *cache, const bd_batch *batch)
 {
-    if (check_cache(cache) != BD_OK || check_batch(batch) != BD_OK || check_heads(n_heads, *cache) != BD_OK)
+    if (check_cache(cache) != BD_OK || check_batch(batch) != BD_OK || check_heads(n_heads, *cache, *batch) != BD_OK)
         return 0;
     return bd::attention_workspace_bytes(n_heads, *cache, *batch);
 }
@@ -695,7 +700,7 @@ bd_status bitdelta_attention(const bd_bf16 *q, int64_t q_stride, int32_t n_heads
 {
     BD_TRY(check_cache(cache));
     BD_TRY(check_batch(batch));
-    BD_TRY(check_heads(n_heads, *cache));
+    BD_TRY(check_heads(n_heads, *cache, *batch));
     if (!(scale > 0.0f) || scale > std::numeric_limits<float>::max())
         return fail(BD_EINVAL, "scale must be positive and finite");
     if (batch->n_tokens == 0)

@@ -1,130 +1,928 @@
 // Causal attention over a paged cache, with shared prefixes
 // (bitdelta_attention).
 //
-// One workgroup per token and query head: its waves take the visible keys in
-// turn, one key per wave and step, each with its own running maximum m, sum l
-// and weighted value o (per key: m' = max(m, s), o = o e^(m - m') + e^(s - m') v),
-// and the waves' states are joined at the end.
+// All kernels keep the running maximum m, sum l and weighted value o of each
+// row (a token and query head) over the keys seen so far,
+//   m' = max(m, s);  l = l 2^(m - m') + sum 2^(s - m');  o likewise with v,
+// s = log2(e) scale q.k, in fp32; the weights 2^(s - m') enter the product
+// with v rounded to bf16 (half a step, 2^-8 relative), as the matrix
+// instructions take them, while l sums them unrounded.  Keys that a row does
+// not see have s = -inf.  States over parts of the keys are joined by the
+// same formula (attention_join).
+//
+// Scores are formed transposed, S' = K Q', so that a lane holds several keys
+// of one row: the maximum and the sum are mostly inside the lane, and the
+// weights are already where the second product O' = V' P' wants its right
+// operand.  The order of the keys in that product is free as long as V' uses
+// the same, so no weight moves between lanes; V' fragments are read from
+// row-major V in LDS by the transposing LDS load.
+//
+// attention_schedule.h says which kernel takes which rows and keys.
+#include <limits.h>
+
+#include "attention_schedule.h"
 #include "bd_device.h"
 #include "decoder_launch.h"
-#include "paged.h"
 
 namespace bd {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 struct AttnArgs {
-    Paged p;
+    Sched s;
     const uint16_t *q;
     const uint8_t *k, *v;
     const float *k_scale, *v_scale;
     uint16_t *out;
+    float *part_o;      // partial states: [rows][head_dim], slots first, then planes
+    float2 *part_ml;    // their m and l
     int64_t q_stride;
-    int32_t n_heads;
     float scale;
 };
 
-template <int N, bool E4M3>
-__device__ __forceinline__ void load_cell(const uint8_t *cache, int64_t at, float *f)
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ bf16x8 as_bf16x8(uint4 w) { return __builtin_bit_cast(bf16x8, w); }
+
+// Four e4m3 numbers as four bf16 (exact).
+__device__ __forceinline__ u32x2 e4m3_to_bf16(uint32_t w)
 {
+    u32x2 r;
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+    return r;
+}
+__device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t a, uint32_t b)
+{
+    const u32x2 x = e4m3_to_bf16(a), y = e4m3_to_bf16(b);
+    return make_uint4(x[0], x[1], y[0], y[1]);
+}
+
+// Position of 16-byte chunk c of row r in a row-major bf16 tile of D columns:
+// a row's chunks are permuted so that both the fragment reads of one column of
+// chunks over 16 rows and the transposing reads of four rows' neighbouring
+// chunks spread over all LDS banks.
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c)
+{
+    const int f = ((r & 3) << 2) | ((r >> 2) & 3);
+    return r * (D / 8) + (c ^ (f & (D / 8 - 1)));
+}
+
+// Transposing LDS read: 16 lanes give the addresses of a 4-row, 16-column
+// block (lane t: row t / 4, columns 4 (t % 4)..), lane t gets column t.
+__device__ __forceinline__ u32x2 read_tr(const uint16_t *p)
+{
+    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)p));
+}
+
+// Keeps LDS accesses of one wave in program order for the compiler; the LDS
+// itself serves a wave's accesses in order.
+__device__ __forceinline__ void lds_order()
+{
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Where a column of V holds a number that is not finite, a weight of zero does
+// not keep it out of the rows that do not see its key.  This takes such
+// numbers out of a fragment and returns them as flags (bf16 ones).
+__device__ __forceinline__ bool split_nonfinite(bf16x8 &v, bf16x8 &flags)
+{
+    uint4 w = __builtin_bit_cast(uint4, v), f;
+    uint32_t *a = &w.x, *b = &f.x;
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (E4M3)
-            f[i] = __builtin_amdgcn_cvt_f32_fp8((int)cache[at + i], 0);
+    for (int i = 0; i < 4; ++i) {
+        const bool lo = (a[i] & 0x7F80u) == 0x7F80u, hi = (a[i] & 0x7F800000u) == 0x7F800000u;
+        any |= lo | hi;
+        b[i] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
+        a[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu);
+    }
+    v = as_bf16x8(w);
+    flags = as_bf16x8(f);
+    return any;
+}
+
+// Exclusive prefix sum over the workgroup's threads, and the total.
+struct Scan {
+    int64_t wave[kWaves];
+};
+__device__ __forceinline__ int64_t scan_block(int64_t v, Scan &sh, int64_t &total)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t y = __shfl_up(x, o);
+        x += lane >= o ? y : 0;
+    }
+    __syncthreads();
+    if (lane == 63)
+        sh.wave[w] = x;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        before += i < w ? sh.wave[i] : 0;
+        total += sh.wave[i];
+    }
+    return before + x - v;
+}
+
+// A list of segments whose sizes are laid end to end: thread i sums the
+// sizes of segments [i * per, (i + 1) * per).
+struct Located {
+    int first;        // a segment at or before the one that holds the position
+    int64_t base;     // where `first` begins
+};
+template <typename Size>
+struct Listing {
+    int n, per;
+    int64_t mine, before, total;
+    __device__ __forceinline__ Listing(int n_, const Size &size, Scan &sh)
+    {
+        n = n_, per = (n + kThreads - 1) / kThreads;
+        mine = 0;
+        const int i0 = threadIdx.x * per;
+        for (int i = i0; i < min(n, i0 + per); ++i)
+            mine += size(i);
+        before = scan_block(mine, sh, total);
+    }
+    // position in [0, total), the same in all threads
+    __device__ __forceinline__ Located locate(int64_t position, Located *sh) const
+    {
+        __syncthreads();
+        if (before <= position && position < before + mine)
+            *sh = {(int)threadIdx.x * per, before};
+        __syncthreads();
+        return *sh;
+    }
+    // where segment i begins
+    __device__ __forceinline__ int64_t begin(int i, const Size &size, Located *sh) const
+    {
+        __syncthreads();
+        if ((int)threadIdx.x == i / per)
+            sh->base = before;
+        __syncthreads();
+        int64_t b = sh->base;
+        for (int j = i / per * per; j < i; ++j)
+            b += size(j);
+        return b;
+    }
+};
+
+// ------------------------------------------------------------ few rows: stream
+//
+// Decode: memory bound.  Each wave streams its own 32-key tiles (every fourth
+// of the workgroup's) straight into registers, K as the fragments that the
+// matrix instruction takes, V by whole rows and on through the wave's own
+// piece of LDS; no barrier until the workgroup's run of one key head ends and
+// the four waves' states are joined.  Eight waves a CU with 16 KB each on the
+// way cover the memory latency.
+template <int D, bool E4M3, int NB>
+__global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
+{
+    constexpr int R = 16 * NB, KS = D / 32, DB = D / 16;
+    constexpr int ES = E4M3 ? 1 : 2;                 // bytes of a cached number
+    constexpr int NK = KS * ES / 2;                  // 16-byte loads of a lane for 16 keys
+    constexpr int LPR = D * ES / 16;                 // lanes that load a row of V
+    constexpr int NV = kStreamKeys * LPR / 64, RPI = 64 / LPR;
+    constexpr int OROW = D + 4;                      // padded row of the join
+    constexpr int kJoin = kWaves * R * OROW * 4, kStage = kWaves * kStreamKeys * D * 2;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kJoin > kStage ? kJoin : kStage];
+    __shared__ float2 wave_ml[kWaves][R];
+    __shared__ Scan scan;
+    __shared__ Located found;
+
+    const Sched &s = a.s;
+    const Paged &p = s.p;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
+    const auto size = [&](int i) { return stream_units(s, i); };
+    const Listing list(p.b.n_seqs, size, scan);
+    const int64_t chunk = stream_chunk(s, list.total), range0 = blockIdx.x * chunk;
+    int64_t at = range0;
+    const int64_t end = min(list.total, at + chunk);
+    if (at >= end)
+        return;
+    const Located loc = list.locate(at, &found);
+    int seq = loc.first;
+    int64_t base = loc.base, units = stream_units(s, seq);
+    uint16_t *vt = reinterpret_cast<uint16_t *>(lds) + wave * kStreamKeys * D;
+    float *oj = reinterpret_cast<float *>(lds);
+
+    while (at < end) {
+        while (base + units <= at) {
+            base += units;
+            units = stream_units(s, ++seq);
+        }
+        const Segment g = sequence(s, seq);
+        const int tiles = key_tiles(g, kStreamKeys), pre_tiles = (int)cdiv(g.pre, kStreamKeys);
+        const int64_t row_tiles = stream_row_tiles(s, g), rows = rows_of(s, g);
+        const int64_t run = (at - base) / tiles;
+        const int t0 = (int)((at - base) - run * tiles), t1 = (int)min((int64_t)tiles, t0 + (end - at));
+        const int head = (int)(run / row_tiles);
+        const int row0 = (int)(run - head * row_tiles) * R;
+        const int32_t *own_table = p.b.page_table + (int64_t)seq * p.b.max_pages;
+        const int32_t *pre_table = g.pre ? p.b.prefix_table + (int64_t)g.group * p.b.max_prefix_pages : own_table;
+
+        bf16x8 q[NB][KS];
+        int seen[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int row = row0 + n * 16 + col, tok = row / s.group;
+            seen[n] = row < rows ? own_seen(g, tok) : 0;
+            const uint16_t *src = a.q + (g.tok0 + (int64_t)tok) * a.q_stride +
+                                  (int64_t)(head * s.group + row - tok * s.group) * D;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                // the columns of a K fragment: those of the lane's 16-byte loads
+                const int c = E4M3 ? (k >> 1) * 64 + quad * 16 + (k & 1) * 8 : k * 32 + quad * 8;
+                q[n][k] = as_bf16x8(row < rows ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0, 0, 0, 0));
+            }
+        }
+        const int least = own_seen(g, row0 / s.group);   // own keys that the first row sees: the fewest
+
+        f32x4 o[NB][DB];
+        float m[NB], l[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            m[n] = -INFINITY, l[n] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                o[n][d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        const float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
+
+        // lane l: the cell of the tile's key l % 32
+        const auto cells = [&](int t) {
+            const bool own = t >= pre_tiles;
+            const int j = (own ? t - pre_tiles : t) * kStreamKeys + (lane & 31);
+            return j < (own ? g.own : g.pre) ? cell_of(p, own ? own_table : pre_table, head, j) : -1;
+        };
+        uint4 kr[2][NK], vr[NV];
+        const auto load = [&](int cell) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int c = __shfl(cell, b * 16 + col);
+                const uint8_t *src = a.k + (int64_t)c * (D * ES) + quad * 16;
+#pragma unroll
+                for (int k = 0; k < NK; ++k)
+                    kr[b][k] = c >= 0 ? *reinterpret_cast<const uint4 *>(src + k * 64) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = __shfl(cell, i * RPI + lane / LPR);
+                vr[i] = c >= 0 ? *reinterpret_cast<const uint4 *>(a.v + (int64_t)c * (D * ES) + lane % LPR * 16)
+                               : make_uint4(0, 0, 0, 0);
+            }
+        };
+        int t = t0 + wave, cell = -1, next = -1;
+        if (t < t1) {
+            cell = cells(t);
+            load(cell);
+        }
+        if (t + kWaves < t1)
+            next = cells(t + kWaves);
+        for (; t < t1; t += kWaves) {
+            const uint32_t held = (uint32_t)__ballot(cell >= 0);
+            lds_order();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int r = i * RPI + lane / LPR, c = lane % LPR;
+                uint4 *dst = reinterpret_cast<uint4 *>(vt);
+                if (E4M3) {
+                    dst[chunk_at<D>(r, 2 * c)] = e4m3x8_to_bf16(vr[i].x, vr[i].y);
+                    dst[chunk_at<D>(r, 2 * c + 1)] = e4m3x8_to_bf16(vr[i].z, vr[i].w);
+                } else {
+                    dst[chunk_at<D>(r, c)] = vr[i];
+                }
+            }
+            f32x4 x[NB][2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    x[n][b] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint4 w = kr[b][E4M3 ? k >> 1 : k];
+                    const bf16x8 kf = as_bf16x8(!E4M3 ? w : k & 1 ? e4m3x8_to_bf16(w.z, w.w) : e4m3x8_to_bf16(w.x, w.y));
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+                        x[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][k], x[n][b], 0, 0, 0);
+                }
+            }
+            // the next tile is on its way while this one is weighed
+            cell = next;
+            if (t + kWaves < t1)
+                load(cell);
+            if (t + 2 * kWaves < t1)
+                next = cells(t + 2 * kWaves);
+
+            const bool own = t >= pre_tiles;
+            const int j0 = own ? (t - pre_tiles) * kStreamKeys : 0;
+            const bool masked = held != 0xFFFFFFFFu || (own && j0 + kStreamKeys > least);
+            bf16x8 pf[NB], sees[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+                if (masked) {
+                    // bit b * 16 + r: key 16 b + 4 quad + r is seen
+                    const int left = own ? seen[n] - j0 : INT_MAX;
+                    uint32_t *w = &ones.x;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int key = b * 16 + quad * 4 + r;
+                            const bool ok = ((held >> key) & 1u) && key < left;
+                            x[n][b][r] = ok ? x[n][b][r] : -INFINITY;
+                            if (!ok)
+                                w[b * 2 + (r >> 1)] &= r & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        }
+                }
+                sees[n] = as_bf16x8(ones);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        mx = fmaxf(mx, x[n][b][r]);
+                mx = fmaxf(mx, __shfl_xor(mx, 16));
+                mx = fmaxf(mx, __shfl_xor(mx, 32)) * sc;
+                const float mn = fmaxf(m[n], mx), mu = mn == -INFINITY ? 0.0f : mn;
+                const float keep = exp2_(m[n] - mu);
+                m[n] = mn;
+                float e[8], sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    e[i] = exp2_(fmaf(x[n][i >> 2][i & 3], sc, -mu));
+                    sum += e[i];
+                }
+                l[n] = fmaf(l[n], keep, sum);
+                pf[n] = as_bf16x8(make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                                             pack_bf16x2(e[6], e[7])));
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    o[n][d] *= keep;
+            }
+            lds_order();
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                // keys 4 quad + 0..3 and 16 + 4 quad + 0..3 of column 16 d + col
+                const int r = quad * 4 + (col >> 2), c = 2 * d + ((col & 3) >> 1), half = (col & 1) * 4;
+                const u32x2 lo = read_tr(vt + chunk_at<D>(r, c) * 8 + half);
+                const u32x2 hi = read_tr(vt + chunk_at<D>(r + 16, c) * 8 + half);
+                bf16x8 vf = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1])), flags;
+                if (masked && __any(split_nonfinite(vf, flags))) {
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        const f32x4 bad = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            flags, sees[n], (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+                        for (int r4 = 0; r4 < 4; ++r4)
+                            o[n][d][r4] = bad[r4] > 0.0f ? NAN : o[n][d][r4];
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[n], o[n][d], 0, 0, 0);
+            }
+        }
+
+        // join the four waves' states
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            l[n] += __shfl_xor(l[n], 16);
+            l[n] += __shfl_xor(l[n], 32);
+            if (quad == 0)
+                wave_ml[wave][n * 16 + col] = make_float2(m[n], l[n]);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                *reinterpret_cast<f32x4 *>(oj + (wave * R + n * 16 + col) * OROW + d * 16 + quad * 4) = o[n][d];
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == tiles;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0 ? 1 : 0);
+        const float vs = E4M3 && a.v_scale ? a.v_scale[head] : 1.0f;
+        for (int u = threadIdx.x; u < R * (D / 4); u += kThreads) {
+            const int r = u / (D / 4), c = u % (D / 4) * 4, row = row0 + r;
+            if (row >= rows)
+                continue;
+            float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                mm = fmaxf(mm, wave_ml[w][r].x);
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float2 ml = wave_ml[w][r];
+                if (ml.x == -INFINITY && !(ml.y != ml.y))
+                    continue;
+                const float e = exp2_(ml.x - mm);
+                ll = fmaf(ml.y, e, ll);
+                acc += *reinterpret_cast<const f32x4 *>(oj + (w * R + r) * OROW + c) * e;
+            }
+            acc *= vs;
+            const int tok = row / s.group;
+            const int64_t cell_out = (g.tok0 + (int64_t)tok) * s.n_heads + head * s.group + row - tok * s.group;
+            if (whole && !g.shared) {
+                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+                u32x2 w;
+                w[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+                w[1] = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+                *reinterpret_cast<u32x2 *>(a.out + cell_out * D + c) = w;
+            } else {
+                const int64_t pr = whole ? 2 * (int64_t)s.stream_wgs * R + cell_out : slot * R + r;
+                *reinterpret_cast<f32x4 *>(a.part_o + pr * D + c) = acc;
+                if (c == 0)
+                    a.part_ml[pr] = make_float2(mm, ll);
+            }
+        }
+        __syncthreads();
+        at += t1 - t0;
+    }
+}
+
+// ------------------------------------------------------------- many rows: tiles
+//
+// Prompts and shared prefixes: matrix bound.  A workgroup holds 128 rows, 32
+// a wave, and walks 64-key tiles of K and V that all four waves read from LDS;
+// a tile's loads are in registers one step ahead, and LDS holds two tiles, so
+// a step has one barrier.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
+{
+    constexpr int KS = D / 16, DB = D / 32;
+    constexpr int ES = E4M3 ? 1 : 2;
+    constexpr int LPR = D * ES / 16;                          // threads that load a row
+    constexpr int NL = kTileKeys * LPR / kThreads;            // loads of a thread, K and V each
+    constexpr int RPI = kThreads / LPR;
+    static_assert(NL >= 1, "a tile is at least one load of every thread");
+    __shared__ __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * D], vt[2][kTileKeys * D];
+    __shared__ uint8_t key_held[2][kTileKeys];
+    __shared__ Scan scan;
+    __shared__ Located found;
+
+    const Sched &s = a.s;
+    const Paged &p = s.p;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
+    const int n_seg = p.b.n_seqs + p.b.n_groups;
+    int64_t depth;
+    {
+        const auto work = [&](int i) {
+            const Segment g = tiled_segment(s, i);
+            return g.ntok ? tiled_work(s, g) : 0;
+        };
+        const Listing<decltype(work)> all(n_seg, work, scan);
+        depth = tiled_depth(s, all.total);
+    }
+    const auto size = [&](int i) { return tiled_items(s, tiled_segment(s, i), depth); };
+    const Listing<decltype(size)> list(n_seg, size, scan);
+
+    for (int64_t item = blockIdx.x; item < list.total; item += gridDim.x) {
+        const Located loc = list.locate(item, &found);
+        int seg = loc.first;
+        int64_t base = loc.base;
+        Segment g;
+        for (;; ++seg) {
+            g = tiled_segment(s, seg);
+            const int64_t n = tiled_items(s, g, depth);
+            if (item < base + n)
+                break;
+            base += n;
+        }
+        // heads fastest, then splits, then row tiles from the last (the longest) to the first
+        const int64_t idx = item - base;
+        const int splits = tiled_splits(s, g, depth);
+        const int head = (int)(idx % p.n_kv), split = (int)(idx / p.n_kv % splits);
+        const int64_t rows = rows_of(s, g);
+        const int row0 = (int)(tiled_row_tiles(s, g) - 1 - idx / p.n_kv / splits) * kTileRows;
+        const int rows_here = (int)min((int64_t)kTileRows, rows - row0);
+        const int pre_tiles = (int)cdiv(g.pre, kTileKeys);
+        const bool is_prefix = seg >= p.b.n_seqs;
+        // tiles up to the last row's own key; a split's share is that of the whole segment
+        const int last_seen = is_prefix ? 0 : own_seen(g, (row0 + rows_here - 1) / s.group);
+        const int per = (int)cdiv(key_tiles(g, kTileKeys), splits);
+        const int t0 = split * per, t1 = min(t0 + per, pre_tiles + (int)cdiv(last_seen, kTileKeys));
+        const int32_t *own_table = is_prefix ? nullptr : p.b.page_table + (int64_t)seg * p.b.max_pages;
+        const int32_t *pre_table = g.pre ? p.b.prefix_table + (int64_t)g.group * p.b.max_prefix_pages : nullptr;
+
+        const int row = row0 + wave * 32 + col, tok = row / s.group;
+        const bool live = row < rows;
+        const int seen = live ? own_seen(g, tok) : 0;
+        const int wave_rows = rows_here - wave * 32;                       // may be negative
+        const int least = own_seen(g, (row0 + wave * 32) / s.group);       // the wave's first row
+        const int most = wave_rows <= 0 ? 0 : own_seen(g, (row0 + min(rows_here, wave * 32 + 32) - 1) / s.group);
+        const int64_t cell_out = (g.tok0 + (int64_t)tok) * s.n_heads + head * s.group + row - tok * s.group;
+        bf16x8 q[KS];
+        {
+            const uint16_t *src = a.q + (g.tok0 + (int64_t)tok) * a.q_stride +
+                                  (int64_t)(head * s.group + row - tok * s.group) * D + half * 8;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                q[k] = as_bf16x8(live ? *reinterpret_cast<const uint4 *>(src + k * 16) : make_uint4(0, 0, 0, 0));
+        }
+        f32x16 o[DB];
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                o[d][r] = 0.0f;
+        const float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
+
+        int cell[NL];
+        uint4 kr[NL], vr[NL];
+        uint32_t held_bits = 0;                                    // of the loads in flight
+        const auto cells = [&](int t) {
+            const bool own = t >= pre_tiles;
+            const int j0 = (own ? t - pre_tiles : t) * kTileKeys + threadIdx.x / LPR, n = own ? g.own : g.pre;
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                cell[i] = j0 + i * RPI < n ? cell_of(p, own ? own_table : pre_table, head, j0 + i * RPI) : -1;
+        };
+        const auto load = [&]() {
+            held_bits = 0;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const bool ok = cell[i] >= 0;
+                const int64_t off = (int64_t)cell[i] * (D * ES) + threadIdx.x % LPR * 16;
+                kr[i] = ok ? *reinterpret_cast<const uint4 *>(a.k + off) : make_uint4(0, 0, 0, 0);
+                vr[i] = ok ? *reinterpret_cast<const uint4 *>(a.v + off) : make_uint4(0, 0, 0, 0);
+                held_bits |= (ok ? 1u : 0u) << i;
+            }
+        };
+        const auto stage = [&](int buf) {
+            uint4 *kd = reinterpret_cast<uint4 *>(kt[buf]), *vd = reinterpret_cast<uint4 *>(vt[buf]);
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int r = i * RPI + threadIdx.x / LPR, c = threadIdx.x % LPR;
+                if (E4M3) {
+                    kd[chunk_at<D>(r, 2 * c)] = e4m3x8_to_bf16(kr[i].x, kr[i].y);
+                    kd[chunk_at<D>(r, 2 * c + 1)] = e4m3x8_to_bf16(kr[i].z, kr[i].w);
+                    vd[chunk_at<D>(r, 2 * c)] = e4m3x8_to_bf16(vr[i].x, vr[i].y);
+                    vd[chunk_at<D>(r, 2 * c + 1)] = e4m3x8_to_bf16(vr[i].z, vr[i].w);
+                } else {
+                    kd[chunk_at<D>(r, c)] = kr[i];
+                    vd[chunk_at<D>(r, c)] = vr[i];
+                }
+                if (c == 0)
+                    key_held[buf][r] = (held_bits >> i) & 1u;
+            }
+        };
+        if (t0 < t1) {
+            cells(t0);
+            load();
+            stage(t0 & 1);
+            if (t0 + 1 < t1) {
+                cells(t0 + 1);
+                load();
+            }
+            if (t0 + 2 < t1)
+                cells(t0 + 2);
+        }
+        __syncthreads();
+        for (int t = t0; t < t1; ++t) {
+            const int buf = t & 1;
+            const bool own = t >= pre_tiles;
+            const int j0 = own ? (t - pre_tiles) * kTileKeys : 0;
+            if (wave_rows > 0 && !(own && j0 >= most)) {
+                const uint64_t held = __ballot(key_held[buf][lane] != 0);
+                f32x16 x[2];
+                const uint4 *kl = reinterpret_cast<const uint4 *>(kt[buf]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        x[b][r] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            as_bf16x8(kl[chunk_at<D>(b * 32 + col, 2 * k + half)]), q[k], x[b], 0, 0, 0);
+                }
+                const bool masked = held != ~0ull || (own && j0 + kTileKeys > least);
+                const int left = own ? seen - j0 : INT_MAX;
+                if (masked) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int key = b * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
+                            x[b][r] = ((held >> key) & 1u) && key < left ? x[b][r] : -INFINITY;
+                        }
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        mx = fmaxf(mx, x[b][r]);
+                mx = fmaxf(mx, __shfl_xor(mx, 32)) * sc;
+                const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.0f : mn;
+                const float keep = exp2_(m - mu);
+                m = mn;
+                float sum = 0.0f;
+                bf16x8 pf[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float e[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        e[r] = exp2_(fmaf(x[i >> 1][(i & 1) * 8 + r], sc, -mu));
+                        sum += e[r];
+                    }
+                    pf[i] = as_bf16x8(make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
+                                                 pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])));
+                }
+                l = fmaf(l, keep, sum);
+                if (__any(keep != 1.0f)) {
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        o[d] *= keep;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // keys 16 i + 4 half + 0..3 and + 8
+                    const int r = i * 16 + half * 4 + ((lane & 15) >> 2);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const int c = d * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), in = (lane & 1) * 4;
+                        const u32x2 lo = read_tr(vt[buf] + chunk_at<D>(r, c) * 8 + in);
+                        const u32x2 hi = read_tr(vt[buf] + chunk_at<D>(r + 8, c) * 8 + in);
+                        bf16x8 vf = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1])), flags;
+                        if (masked && __any(split_nonfinite(vf, flags))) {
+                            uint4 ones = make_uint4(0, 0, 0, 0);
+                            uint32_t *w = &ones.x;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int key = i * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
+                                if (((held >> key) & 1u) && key < left)
+                                    w[e >> 1] |= e & 1 ? 0x3F800000u : 0x3F80u;
+                            }
+                            f32x16 bad;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                bad[e] = 0.0f;
+                            bad = __builtin_amdgcn_mfma_f32_32x32x16_bf16(flags, as_bf16x8(ones), bad, 0, 0, 0);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[d][e] = bad[e] > 0.0f ? NAN : o[d][e];
+                        }
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[i], o[d], 0, 0, 0);
+                    }
+                }
+            }
+            if (t + 1 < t1) {
+                stage(buf ^ 1);
+                if (t + 2 < t1)
+                    load();
+                if (t + 3 < t1)
+                    cells(t + 3);
+            }
+            __syncthreads();
+        }
+
+        l += __shfl_xor(l, 32);
+        if (live) {
+            const float vs = E4M3 && a.v_scale ? a.v_scale[head] : 1.0f;
+            const bool whole = splits == 1 && !g.shared;
+            const float f = whole ? (l == 0.0f ? 0.0f : vs / l) : vs;
+            const int64_t plane = is_prefix ? s.splits + split : split;
+            const int64_t pr = 2 * (int64_t)s.stream_wgs * s.stream_rows +
+                               plane * s.p.b.n_tokens * s.n_heads + cell_out;
+            if (!whole && half == 0)
+                a.part_ml[pr] = make_float2(m, l);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int c = d * 32 + r * 8 + half * 4;
+                    const f32x4 w = {o[d][4 * r] * f, o[d][4 * r + 1] * f, o[d][4 * r + 2] * f, o[d][4 * r + 3] * f};
+                    if (whole) {
+                        u32x2 b;
+                        b[0] = pack_bf16x2(w[0], w[1]);
+                        b[1] = pack_bf16x2(w[2], w[3]);
+                        *reinterpret_cast<u32x2 *>(a.out + cell_out * D + c) = b;
+                    } else {
+                        *reinterpret_cast<f32x4 *>(a.part_o + pr * D + c) = w;
+                    }
+                }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------ join
+//
+// Joins the partial states of a token's heads, one wave a head; writes the
+// zero rows of tokens that see nothing; leaves finished rows alone.
+template <int D>
+__global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
+{
+    constexpr int N = D / 64;
+    __shared__ Scan scan;
+    __shared__ Located found;
+    const Sched &s = a.s;
+    const Paged &p = s.p;
+    const int64_t tok = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t slots = 2 * (int64_t)s.stream_wgs * s.stream_rows, plane = p.b.n_tokens * s.n_heads;
+
+    const int seq = seq_of(p, tok);
+    // parts of own keys: planes [0, own_parts), or the slots of workgroups first_wg .. where `slotted`
+    int own_parts = 0, prefix_parts = 0;
+    bool by_stream = false;
+    Segment g;
+    int64_t units0 = 0, chunk = 1;
+    if (seq >= 0) {
+        g = sequence(s, seq);
+        by_stream = streamed(s, g);
+        const int64_t none = 0;
+        if (s.tiled && (g.shared || (!by_stream && s.splits > 1))) {
+            const int n_seg = p.b.n_seqs + p.b.n_groups;
+            const auto work = [&](int i) {
+                const Segment q = tiled_segment(s, i);
+                return q.ntok ? tiled_work(s, q) : none;
+            };
+            const Listing<decltype(work)> all(n_seg, work, scan);
+            const int64_t depth = tiled_depth(s, all.total);
+            if (!by_stream)
+                own_parts = tiled_splits(s, g, depth);
+            if (g.shared)
+                prefix_parts = tiled_splits(s, prefix(s, g.group), depth);
+        } else if (!by_stream) {
+            own_parts = 1;
+        }
+        if (!by_stream && own_parts == 1 && !g.shared)
+            return;
+        if (by_stream) {
+            const auto size = [&](int i) { return stream_units(s, i); };
+            const Listing<decltype(size)> list(p.b.n_seqs, size, scan);
+            chunk = stream_chunk(s, list.total);
+            units0 = list.begin(seq, size, &found);
+        }
+    }
+    const int tiles = seq >= 0 ? key_tiles(g, kStreamKeys) : 0;
+    for (int h = blockIdx.y * kWaves + wave; h < s.n_heads; h += gridDim.y * kWaves) {
+        const int64_t cell_out = tok * s.n_heads + h;
+        int64_t first_wg = 0, row_in = 0;
+        int parts = own_parts;
+        bool slotted = false;
+        if (by_stream && tiles) {
+            const int head = h / s.group;
+            const int64_t row = (tok - g.tok0) * s.group + h - head * s.group;
+            const int64_t u0 = units0 + (head * stream_row_tiles(s, g) + row / s.stream_rows) * tiles;
+            first_wg = u0 / chunk;
+            parts = (int)((u0 + tiles - 1) / chunk - first_wg) + 1;
+            slotted = parts > 1;
+            row_in = row % s.stream_rows;
+            if (!slotted && !g.shared)
+                continue;
+        }
+        float m = -INFINITY, l = 0.0f, o[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            o[i] = 0.0f;
+        const int total = parts + prefix_parts;
+        for (int b = 0; b < total; b += 64) {
+            const int i = b + lane;
+            int64_t pr = 0;
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (i < total) {
+                if (i >= parts)
+                    pr = slots + (s.splits + i - parts) * plane + cell_out;
+                else if (slotted)
+                    pr = (2 * (first_wg + i) + (i == 0 ? 1 : 0)) * s.stream_rows + row_in;
+                else
+                    pr = slots + i * plane + cell_out;
+                ml = a.part_ml[pr];
+            }
+            float mx = ml.x;
+#pragma unroll
+            for (int w = 32; w > 0; w >>= 1)
+                mx = fmaxf(mx, __shfl_xor(mx, w));
+            const float mn = fmaxf(m, mx);
+            // a part without keys has m = -inf and l = 0 (NaN where its scores were)
+            const bool none = ml.x == -INFINITY && !(ml.y != ml.y);
+            const float e = none ? 0.0f : exp2_(ml.x - mn), keep = m == -INFINITY ? 0.0f : exp2_(m - mn);
+            float sum = none ? 0.0f : e * ml.y;
+#pragma unroll
+            for (int w = 32; w > 0; w >>= 1)
+                sum += __shfl_xor(sum, w);
+            l = l * keep + sum;
+            m = mn;
+#pragma unroll
+            for (int i2 = 0; i2 < N; ++i2)
+                o[i2] *= keep;
+            // eight states' loads in flight; lanes past the last part hold `none` and row 0
+            for (int j = 0; j < min(64, total - b); j += 8)
+#pragma unroll
+                for (int j8 = 0; j8 < 8; ++j8) {
+                    const float ej = __shfl(e, j + j8);
+                    const int64_t row = __shfl(pr, j + j8);
+                    const bool skip = __shfl((int)none, j + j8);
+                    const float *src = a.part_o + row * D + lane * N;
+#pragma unroll
+                    for (int i2 = 0; i2 < N; ++i2)
+                        o[i2] += skip ? 0.0f : ej * src[i2];
+                }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (N == 2)
+            *reinterpret_cast<uint32_t *>(a.out + cell_out * D + lane * 2) = pack_bf16x2(o[0] * inv, o[N - 1] * inv);
         else
-            f[i] = lo_f32(reinterpret_cast<const uint16_t *>(cache)[at + i]);
+            a.out[cell_out * D + lane] = to_bf16(o[0] * inv);
+    }
+}
+
+// ------------------------------------------------------------------------ host
+
+struct Plan {
+    Sched s;
+    int64_t tiled_grid, rows;     // rows of partial states
+};
+
+Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
+{
+    Plan pl;
+    Sched &s = pl.s;
+    s.p = {b, c.n_pages, c.n_kv_heads, __builtin_ctz((unsigned)c.page_size)};
+    s.n_heads = n_heads, s.group = n_heads / c.n_kv_heads;
+    const int64_t T = b.n_tokens;
+    // 32 rows a streaming tile; 16 where the hint says that no sequence has more
+    const int64_t most = b.max_new > 0 ? (int64_t)b.max_new * s.group : T > b.n_seqs ? INT_MAX : s.group;
+    s.stream_rows = most <= 16 ? 16 : 32;
+    s.tiled = b.n_groups > 0 || most > 32;
+    s.few = s.tiled ? 32 : INT_MAX;
+    s.stream_wgs = 512;
+    // enough splits that row tiles x key heads x splits fill the chip one and a half times
+    const int64_t tiles = cdiv(T * s.group, kTileRows) * c.n_kv_heads;
+    const int64_t want = cdiv(768, tiles);
+    s.splits = s.tiled ? (int32_t)(want < 1 ? 1 : want > 64 ? 64 : want) : 1;
+    const int64_t planes = b.n_groups > 0 ? 2 * s.splits : s.splits > 1 ? s.splits : 0;
+    pl.rows = 2 * (int64_t)s.stream_wgs * s.stream_rows + planes * T * n_heads;
+    const int64_t segs = (b.n_seqs < T ? b.n_seqs : T) + (b.n_groups < T ? b.n_groups : T);
+    const int64_t most_items = (2 * (T * s.group / kTileRows) + segs) * c.n_kv_heads + kTiledSlots;
+    pl.tiled_grid = most_items < 8192 ? most_items : 8192;
+    return pl;
 }
 
 template <int D, bool E4M3>
-__global__ __launch_bounds__(kWaves * 64) void attention_rows(AttnArgs a)
+void start(const AttnArgs &a, const Plan &pl, hipStream_t st)
 {
-    constexpr int N = D / 64;
-    __shared__ float ml[kWaves][2], os[kWaves][D];
-    const Paged &p = a.p;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y, kvh = h / (a.n_heads / p.n_kv);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int s = seq_of(p, t);
-    int seen[2] = {0, 0};
-    const int32_t *table[2] = {p.b.prefix_table, p.b.page_table};
-    if (s >= 0) {
-        seen[1] = max(0, own_keys(p, s) - (seq_begin(p, s + 1) - (int)t) + 1);
-        table[1] += (int64_t)s * p.b.max_pages;
-        const int g = group_of(p, s);
-        if (g >= 0) {
-            seen[0] = prefix_keys(p, g);
-            table[0] += (int64_t)g * p.b.max_prefix_pages;
-        }
-    }
-    const float scale = a.scale * (E4M3 && a.k_scale ? a.k_scale[kvh] : 1.0f);
-    float q[N], o[N] = {}, m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < N; ++i)
-        q[i] = lo_f32(a.q[t * a.q_stride + h * D + lane * N + i]) * scale;
-    for (int part = 0; part < 2; ++part)
-        for (int j = wave; j < seen[part]; j += kWaves) {
-            const int page = table[part][j >> p.page_shift];
-            if ((unsigned)page >= (unsigned)p.n_pages)
-                continue;
-            const int64_t at = (((((int64_t)page * p.n_kv + kvh) << p.page_shift) +
-                                 (j & ((1 << p.page_shift) - 1))) * D) + lane * N;
-            float k[N], v[N], x = 0.0f;
-            load_cell<N, E4M3>(a.k, at, k);
-            load_cell<N, E4M3>(a.v, at, v);
-            for (int i = 0; i < N; ++i)
-                x = fmaf(q[i], k[i], x);
-            for (int w = 32; w > 0; w >>= 1)
-                x += __shfl_xor(x, w);
-            const float mn = fmaxf(m, x);
-            const float keep = m == mn ? 1.0f : __expf(m - mn), e = x == mn ? 1.0f : __expf(x - mn);
-            m = mn;
-            l = l * keep + e;
-            for (int i = 0; i < N; ++i)
-                o[i] = o[i] * keep + e * v[i];
-        }
-    if (lane == 0)
-        ml[wave][0] = m, ml[wave][1] = l;
-    for (int i = 0; i < N; ++i)
-        os[wave][lane * N + i] = o[i];
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float mm = -INFINITY, ll = 0.0f, oo = 0.0f;
-        for (int w = 0; w < kWaves; ++w)
-            mm = fmaxf(mm, ml[w][0]);
-        for (int w = 0; w < kWaves; ++w) {
-            const float e = ml[w][0] == -INFINITY ? 0.0f : __expf(ml[w][0] - mm);
-            ll += e * ml[w][1];
-            oo += e * os[w][threadIdx.x];
-        }
-        const float vs = E4M3 && a.v_scale ? a.v_scale[kvh] : 1.0f;
-        a.out[(t * a.n_heads + h) * D + threadIdx.x] = to_bf16(ll > 0.0f || ll != ll ? oo / ll * vs : 0.0f);
-    }
+    const Sched &s = a.s;
+    if (s.tiled)
+        attention_tiled<D, E4M3><<<dim3((unsigned)pl.tiled_grid), kThreads, 0, st>>>(a);
+    if (s.stream_rows == 16)
+        attention_stream<D, E4M3, 1><<<dim3(s.stream_wgs), kThreads, 0, st>>>(a);
+    else
+        attention_stream<D, E4M3, 2><<<dim3(s.stream_wgs), kThreads, 0, st>>>(a);
+    const int64_t T = s.p.b.n_tokens, waves = (s.n_heads + kWaves - 1) / kWaves;
+    const int64_t y = 1024 / T;
+    attention_join<D><<<dim3((unsigned)T, (unsigned)(y < 1 ? 1 : y > waves ? waves : y)), kThreads, 0, st>>>(a);
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int32_t, const bd_kv_cache &, const bd_batch &) { return 0; }
+size_t attention_workspace_bytes(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
+{
+    if (b.n_tokens == 0)
+        return 0;
+    return (size_t)make_plan(n_heads, c, b).rows * (c.head_dim * 4 + 8);
+}
 
 hipError_t launch_attention(const uint16_t *q, int64_t q_stride, int32_t n_heads, float scale, const bd_kv_cache &c,
-                            const bd_batch &b, uint16_t *out, void *, hipStream_t s)
+                            const bd_batch &b, uint16_t *out, void *workspace, hipStream_t st)
 {
+    const Plan pl = make_plan(n_heads, c, b);
     AttnArgs a;
-    a.p = {b, c.n_pages, c.n_kv_heads, __builtin_ctz((unsigned)c.page_size)};
-    a.q = q, a.q_stride = q_stride, a.out = out, a.n_heads = n_heads, a.scale = scale;
+    a.s = pl.s;
+    a.q = q, a.q_stride = q_stride, a.out = out, a.scale = scale;
     a.k = static_cast<const uint8_t *>(c.k), a.v = static_cast<const uint8_t *>(c.v);
     a.k_scale = c.k_scale, a.v_scale = c.v_scale;
-    const dim3 grid((unsigned)b.n_tokens, (unsigned)n_heads);
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + pl.rows * c.head_dim);
     const bool e4m3 = c.dtype == BD_KV_E4M3;
     if (c.head_dim == 64) {
         if (e4m3)
-            attention_rows<64, true><<<grid, kWaves * 64, 0, s>>>(a);
+            start<64, true>(a, pl, st);
         else
-            attention_rows<64, false><<<grid, kWaves * 64, 0, s>>>(a);
+            start<64, false>(a, pl, st);
     } else {
         if (e4m3)
-            attention_rows<128, true><<<grid, kWaves * 64, 0, s>>>(a);
+            start<128, true>(a, pl, st);
         else
-            attention_rows<128, false><<<grid, kWaves * 64, 0, s>>>(a);
+            start<128, false>(a, pl, st);
     }
     return hipGetLastError();
 }

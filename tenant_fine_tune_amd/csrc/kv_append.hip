@@ -70,15 +70,13 @@ __global__ __launch_bounds__(kThreads) void append_tokens(AppendArgs a)
     const int64_t t = blockIdx.x;
     const int s = seq_of(p, t);
     bool placed = s >= 0;
-    int64_t cell = -1;   // page * n_kv * page_size + slot: the cell of head 0
+    int64_t cell = -1;   // of head 0
     if (placed) {
         const int at = own_keys(p, s) - (seq_begin(p, s + 1) - (int)t);
         placed = at >= 0;
         const int g = group_of(p, s);
         if (placed) {
-            const int page = p.b.page_table[(int64_t)s * p.b.max_pages + (at >> p.page_shift)];
-            if ((unsigned)page < (unsigned)p.n_pages)
-                cell = (((int64_t)page * p.n_kv) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
+            cell = cell_of(p, p.b.page_table + (int64_t)s * p.b.max_pages, 0, at);
             const double pos = (double)at + (g >= 0 ? prefix_keys(p, g) : 0);
             for (int i = threadIdx.x; i < a.rotary / 2; i += kThreads) {
                 // turns, to the nearest whole one, then radians / pi in [-1, 1]
