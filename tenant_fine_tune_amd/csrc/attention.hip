@@ -30,6 +30,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kSchedMfma = 0x008, kSchedLdsRead = 0x100;   // masks of sched_group_barrier
 
 struct AttnArgs {
     Sched s;
@@ -62,16 +63,16 @@ __device__ __forceinline__ uint4 e4m3x8_to_bf16(uint32_t a, uint32_t b)
     return make_uint4(x[0], x[1], y[0], y[1]);
 }
 
-// Position of 16-byte chunk c of row r in a row-major bf16 tile of D columns:
-// a row's chunks are permuted so that both the fragment reads of one column of
-// chunks over 16 rows and the transposing reads of four rows' neighbouring
-// chunks spread over all LDS banks.
+// Row strides of bf16 tiles in LDS, in numbers: the padding shifts a row
+// against the one before by 4 banks (K: 16 rows' 16-byte pieces of one column
+// block), 16 banks (V of the tiled kernel: four rows' 64 bytes) or 8 banks (V
+// of the streaming kernel: eight rows' 32 bytes), so that one access touches
+// every bank equally often; a fixed stride keeps all addresses of a tile at
+// one register plus constants.
 template <int D>
-__device__ __forceinline__ int chunk_at(int r, int c)
-{
-    const int f = ((r & 3) << 2) | ((r >> 2) & 3);
-    return r * (D / 8) + (c ^ (f & (D / 8 - 1)));
-}
+struct Stride {
+    static constexpr int k = D + 8, v = D + 32, v_stream = D + 16;
+};
 
 // Transposing LDS read: 16 lanes give the addresses of a 4-row, 16-column
 // block (lane t: row t / 4, columns 4 (t % 4)..), lane t gets column t.
@@ -92,24 +93,25 @@ __device__ __forceinline__ void lds_order()
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Where a column of V holds a number that is not finite, a weight of zero does
-// not keep it out of the rows that do not see its key.  This takes such
-// numbers out of a fragment and returns them as flags (bf16 ones).
-__device__ __forceinline__ bool split_nonfinite(bf16x8 &v, bf16x8 &flags)
+// not keep it out of the rows that do not see its key.  In tiles that some of
+// the rows see only in part such numbers are therefore taken out of V, and the
+// rows that do see them are set to NaN afterwards.  This clears them in eight
+// bf16 numbers and returns which they were.
+__device__ __forceinline__ uint32_t take_nonfinite(uint4 &w)
 {
-    uint4 w = __builtin_bit_cast(uint4, v), f;
-    uint32_t *a = &w.x, *b = &f.x;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool lo = (a[i] & 0x7F80u) == 0x7F80u, hi = (a[i] & 0x7F800000u) == 0x7F800000u;
-        any |= lo | hi;
-        b[i] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
-        a[i] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0xFFFFu : 0xFFFFFFFFu);
-    }
-    v = as_bf16x8(w);
-    flags = as_bf16x8(f);
-    return any;
+    uint32_t bits = 0;
+    const auto one = [&](uint32_t &x, int i) {
+        if ((x & 0x7F80u) == 0x7F80u)
+            x &= 0xFFFF0000u, bits |= 1u << (2 * i);
+        if ((x & 0x7F800000u) == 0x7F800000u)
+            x &= 0xFFFFu, bits |= 2u << (2 * i);
+    };
+    one(w.x, 0), one(w.y, 1), one(w.z, 2), one(w.w, 3);
+    return bits;
 }
+
+// The lowest n bits (none for n < 0, all from 64 on).
+__device__ __forceinline__ uint64_t first_bits64(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
 // Exclusive prefix sum over the workgroup's threads, and the total.
 struct Scan {
@@ -196,9 +198,11 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
     constexpr int NK = KS * ES / 2;                  // 16-byte loads of a lane for 16 keys
     constexpr int LPR = D * ES / 16;                 // lanes that load a row of V
     constexpr int NV = kStreamKeys * LPR / 64, RPI = 64 / LPR;
+    constexpr int VS = Stride<D>::v_stream;
     constexpr int OROW = D + 4;                      // padded row of the join
-    constexpr int kJoin = kWaves * R * OROW * 4, kStage = kWaves * kStreamKeys * D * 2;
+    constexpr int kJoin = kWaves * R * OROW * 4, kStage = kWaves * kStreamKeys * VS * 2;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kJoin > kStage ? kJoin : kStage];
+    __shared__ uint8_t bad[kWaves][kStreamKeys][D / 8];
     __shared__ float2 wave_ml[kWaves][R];
     __shared__ Scan scan;
     __shared__ Located found;
@@ -216,7 +220,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
     const Located loc = list.locate(at, &found);
     int seq = loc.first;
     int64_t base = loc.base, units = stream_units(s, seq);
-    uint16_t *vt = reinterpret_cast<uint16_t *>(lds) + wave * kStreamKeys * D;
+    uint16_t *vt = reinterpret_cast<uint16_t *>(lds) + wave * kStreamKeys * VS;
     float *oj = reinterpret_cast<float *>(lds);
 
     while (at < end) {
@@ -269,20 +273,22 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
             return j < (own ? g.own : g.pre) ? cell_of(p, own ? own_table : pre_table, head, j) : -1;
         };
         uint4 kr[2][NK], vr[NV];
+        uint32_t v_held = 0;
+        // a key without a cell reads cell 0: its score is masked, its value cleared
         const auto load = [&](int cell) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int c = __shfl(cell, b * 16 + col);
-                const uint8_t *src = a.k + (int64_t)c * (D * ES) + quad * 16;
+                const uint8_t *src = a.k + (uint64_t)max(__shfl(cell, b * 16 + col), 0) * (D * ES) + quad * 16;
 #pragma unroll
                 for (int k = 0; k < NK; ++k)
-                    kr[b][k] = c >= 0 ? *reinterpret_cast<const uint4 *>(src + k * 64) : make_uint4(0, 0, 0, 0);
+                    kr[b][k] = *reinterpret_cast<const uint4 *>(src + k * 64);
             }
+            v_held = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = __shfl(cell, i * RPI + lane / LPR);
-                vr[i] = c >= 0 ? *reinterpret_cast<const uint4 *>(a.v + (int64_t)c * (D * ES) + lane % LPR * 16)
-                               : make_uint4(0, 0, 0, 0);
+                vr[i] = *reinterpret_cast<const uint4 *>(a.v + (uint64_t)max(c, 0) * (D * ES) + lane % LPR * 16);
+                v_held |= c >= 0 ? 1u << i : 0u;
             }
         };
         int t = t0 + wave, cell = -1, next = -1;
@@ -294,16 +300,27 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
             next = cells(t + kWaves);
         for (; t < t1; t += kWaves) {
             const uint32_t held = (uint32_t)__ballot(cell >= 0);
+            const bool own = t >= pre_tiles;
+            const int j0 = own ? (t - pre_tiles) * kStreamKeys : 0;
+            const bool masked = held != 0xFFFFFFFFu || (own && j0 + kStreamKeys > least);
+            uint32_t any_bad = 0;
             lds_order();
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int r = i * RPI + lane / LPR, c = lane % LPR;
-                uint4 *dst = reinterpret_cast<uint4 *>(vt);
-                if (E4M3) {
-                    dst[chunk_at<D>(r, 2 * c)] = e4m3x8_to_bf16(vr[i].x, vr[i].y);
-                    dst[chunk_at<D>(r, 2 * c + 1)] = e4m3x8_to_bf16(vr[i].z, vr[i].w);
-                } else {
-                    dst[chunk_at<D>(r, c)] = vr[i];
+                const int r = i * RPI + lane / LPR, c = lane % LPR * (E4M3 ? 2 : 1);
+                uint4 w[2] = {vr[i], vr[i]};
+                if (E4M3)
+                    w[0] = e4m3x8_to_bf16(vr[i].x, vr[i].y), w[1] = e4m3x8_to_bf16(vr[i].z, vr[i].w);
+#pragma unroll
+                for (int e = 0; e < (E4M3 ? 2 : 1); ++e) {
+                    if (masked) {
+                        if (!((v_held >> i) & 1u))
+                            w[e] = make_uint4(0, 0, 0, 0);
+                        const uint32_t bits = take_nonfinite(w[e]);
+                        bad[wave][r][c + e] = (uint8_t)bits;
+                        any_bad |= bits;
+                    }
+                    *reinterpret_cast<uint4 *>(vt + r * VS + (c + e) * 8) = w[e];
                 }
             }
             f32x4 x[NB][2];
@@ -328,29 +345,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
             if (t + 2 * kWaves < t1)
                 next = cells(t + 2 * kWaves);
 
-            const bool own = t >= pre_tiles;
-            const int j0 = own ? (t - pre_tiles) * kStreamKeys : 0;
-            const bool masked = held != 0xFFFFFFFFu || (own && j0 + kStreamKeys > least);
-            bf16x8 pf[NB], sees[NB];
+            bf16x8 pf[NB];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
                 if (masked) {
-                    // bit b * 16 + r: key 16 b + 4 quad + r is seen
-                    const int left = own ? seen[n] - j0 : INT_MAX;
-                    uint32_t *w = &ones.x;
+                    const uint32_t ok = (held & (uint32_t)first_bits64(own ? seen[n] - j0 : INT_MAX)) >> quad * 4;
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int key = b * 16 + quad * 4 + r;
-                            const bool ok = ((held >> key) & 1u) && key < left;
-                            x[n][b][r] = ok ? x[n][b][r] : -INFINITY;
-                            if (!ok)
-                                w[b * 2 + (r >> 1)] &= r & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                        }
+                        for (int r = 0; r < 4; ++r)
+                            x[n][b][r] = (ok >> (b * 16 + r)) & 1u ? x[n][b][r] : -INFINITY;
                 }
-                sees[n] = as_bf16x8(ones);
                 float mx = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -379,23 +384,26 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 // keys 4 quad + 0..3 and 16 + 4 quad + 0..3 of column 16 d + col
-                const int r = quad * 4 + (col >> 2), c = 2 * d + ((col & 3) >> 1), half = (col & 1) * 4;
-                const u32x2 lo = read_tr(vt + chunk_at<D>(r, c) * 8 + half);
-                const u32x2 hi = read_tr(vt + chunk_at<D>(r + 16, c) * 8 + half);
-                bf16x8 vf = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1])), flags;
-                if (masked && __any(split_nonfinite(vf, flags))) {
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        const f32x4 bad = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            flags, sees[n], (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-#pragma unroll
-                        for (int r4 = 0; r4 < 4; ++r4)
-                            o[n][d][r4] = bad[r4] > 0.0f ? NAN : o[n][d][r4];
-                    }
-                }
+                const uint16_t *src = vt + (quad * 4 + (col >> 2)) * VS + d * 16 + (col & 3) * 4;
+                const u32x2 lo = read_tr(src), hi = read_tr(src + 16 * VS);
+                const bf16x8 vf = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1]));
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
                     o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[n], o[n][d], 0, 0, 0);
+            }
+            if (masked && __any(any_bad != 0)) {
+#pragma unroll 1
+                for (int key = 0; key < kStreamKeys; ++key)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const int bits = bad[wave][key][2 * d + (quad >> 1)] >> (quad & 1) * 4;
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (((bits >> r) & 1) && (!own || key < seen[n] - j0))
+                                    o[n][d][r] = NAN;
+                    }
             }
         }
 
@@ -469,8 +477,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
     constexpr int NL = kTileKeys * LPR / kThreads;            // loads of a thread, K and V each
     constexpr int RPI = kThreads / LPR;
     static_assert(NL >= 1, "a tile is at least one load of every thread");
-    __shared__ __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * D], vt[2][kTileKeys * D];
-    __shared__ uint8_t key_held[2][kTileKeys];
+    constexpr int KR = Stride<D>::k, VR = Stride<D>::v;
+    __shared__ __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * KR], vt[2][kTileKeys * VR];
+    __shared__ uint8_t key_held[2][kTileKeys], bad[2][kTileKeys][D / 8];
+    __shared__ uint32_t any_bad[2][kWaves];
     __shared__ Scan scan;
     __shared__ Located found;
 
@@ -523,6 +533,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
         const int seen = live ? own_seen(g, tok) : 0;
         const int wave_rows = rows_here - wave * 32;                       // may be negative
         const int least = own_seen(g, (row0 + wave * 32) / s.group);       // the wave's first row
+        const int least_all = own_seen(g, row0 / s.group);
         const int most = wave_rows <= 0 ? 0 : own_seen(g, (row0 + min(rows_here, wave * 32 + 32) - 1) / s.group);
         const int64_t cell_out = (g.tok0 + (int64_t)tok) * s.n_heads + head * s.group + row - tok * s.group;
         bf16x8 q[KS];
@@ -542,85 +553,153 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
                 o[d][r] = 0.0f;
         const float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
 
-        int cell[NL];
-        uint4 kr[NL], vr[NL];
-        uint32_t held_bits = 0;                                    // of the loads in flight
-        const auto cells = [&](int t) {
+        // One set of registers carries K of the next tile until the scores of
+        // this one are done, then its V.  A key without a cell reads cell 0: its
+        // score is masked, its value cleared.
+        int page[NL], cell[NL];
+        uint4 in[NL];
+        const auto tile_keys = [&](int t, int &j0) {
             const bool own = t >= pre_tiles;
-            const int j0 = (own ? t - pre_tiles : t) * kTileKeys + threadIdx.x / LPR, n = own ? g.own : g.pre;
+            j0 = (own ? t - pre_tiles : t) * kTileKeys + threadIdx.x / LPR;
+            return own ? g.own : g.pre;
+        };
+        const auto read_pages = [&](int t) {
+            int j0;
+            const int n = tile_keys(t, j0);
+            const int32_t *table = t >= pre_tiles ? own_table : pre_table;
 #pragma unroll
             for (int i = 0; i < NL; ++i)
-                cell[i] = j0 + i * RPI < n ? cell_of(p, own ? own_table : pre_table, head, j0 + i * RPI) : -1;
+                page[i] = table[min(j0 + i * RPI, n - 1) >> p.page_shift];
         };
-        const auto load = [&]() {
-            held_bits = 0;
+        const auto load = [&](const uint8_t *cache) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                in[i] = *reinterpret_cast<const uint4 *>(cache + (uint64_t)max(cell[i], 0) * (D * ES) +
+                                                         threadIdx.x % LPR * 16);
+        };
+        const auto load_k = [&](int t) {
+            int j0;
+            const int n = tile_keys(t, j0);
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
-                const bool ok = cell[i] >= 0;
-                const int64_t off = (int64_t)cell[i] * (D * ES) + threadIdx.x % LPR * 16;
-                kr[i] = ok ? *reinterpret_cast<const uint4 *>(a.k + off) : make_uint4(0, 0, 0, 0);
-                vr[i] = ok ? *reinterpret_cast<const uint4 *>(a.v + off) : make_uint4(0, 0, 0, 0);
-                held_bits |= (ok ? 1u : 0u) << i;
+                const int j = j0 + i * RPI;
+                cell[i] = j < n && (unsigned)page[i] < (unsigned)p.n_pages
+                              ? ((page[i] * p.n_kv + head) << p.page_shift) + (j & ((1 << p.page_shift) - 1)) : -1;
+            }
+            load(a.k);
+        };
+        // some row of the workgroup does not see all of tile t's keys that others see
+        const auto partial = [&](int t) { return t >= pre_tiles && (t - pre_tiles + 1) * kTileKeys > least_all; };
+        const int ldr = threadIdx.x / LPR, ldc = threadIdx.x % LPR * (E4M3 ? 2 : 1);
+        const auto stage_k = [&](int t) {
+            uint16_t *dst = kt[t & 1] + ldr * KR + ldc * 8;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                uint4 *w = reinterpret_cast<uint4 *>(dst + i * RPI * KR);
+                if (E4M3)
+                    w[0] = e4m3x8_to_bf16(in[i].x, in[i].y), w[1] = e4m3x8_to_bf16(in[i].z, in[i].w);
+                else
+                    w[0] = in[i];
+                if (ldc == 0)
+                    key_held[t & 1][ldr + i * RPI] = cell[i] >= 0;
             }
         };
-        const auto stage = [&](int buf) {
-            uint4 *kd = reinterpret_cast<uint4 *>(kt[buf]), *vd = reinterpret_cast<uint4 *>(vt[buf]);
+        const auto stage_v = [&](int t) {
+            const int buf = t & 1;
+            uint16_t *dst = vt[buf] + ldr * VR + ldc * 8;
+            const bool check = partial(t);
+            uint32_t found_bad = 0;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
-                const int r = i * RPI + threadIdx.x / LPR, c = threadIdx.x % LPR;
-                if (E4M3) {
-                    kd[chunk_at<D>(r, 2 * c)] = e4m3x8_to_bf16(kr[i].x, kr[i].y);
-                    kd[chunk_at<D>(r, 2 * c + 1)] = e4m3x8_to_bf16(kr[i].z, kr[i].w);
-                    vd[chunk_at<D>(r, 2 * c)] = e4m3x8_to_bf16(vr[i].x, vr[i].y);
-                    vd[chunk_at<D>(r, 2 * c + 1)] = e4m3x8_to_bf16(vr[i].z, vr[i].w);
-                } else {
-                    kd[chunk_at<D>(r, c)] = kr[i];
-                    vd[chunk_at<D>(r, c)] = vr[i];
+                uint4 v[2] = {in[i], in[i]};
+                if (E4M3)
+                    v[0] = e4m3x8_to_bf16(in[i].x, in[i].y), v[1] = e4m3x8_to_bf16(in[i].z, in[i].w);
+#pragma unroll
+                for (int e = 0; e < (E4M3 ? 2 : 1); ++e) {
+                    if (cell[i] < 0)
+                        v[e] = make_uint4(0, 0, 0, 0);
+                    if (check) {
+                        const uint32_t bits = take_nonfinite(v[e]);
+                        bad[buf][ldr + i * RPI][ldc + e] = (uint8_t)bits;
+                        found_bad |= bits;
+                    }
+                    reinterpret_cast<uint4 *>(dst + i * RPI * VR)[e] = v[e];
                 }
-                if (c == 0)
-                    key_held[buf][r] = (held_bits >> i) & 1u;
+            }
+            if (check) {
+                const bool any = __any(found_bad != 0);
+                if (lane == 0)
+                    any_bad[buf][wave] = any;
             }
         };
+        // q has to be there before the loop: its wait inside would be one for all loads in flight
+        wait_vmcnt<0>();
         if (t0 < t1) {
-            cells(t0);
-            load();
-            stage(t0 & 1);
-            if (t0 + 1 < t1) {
-                cells(t0 + 1);
-                load();
-            }
+            read_pages(t0);
+            load_k(t0);
+            stage_k(t0);
+            load(a.v);
+            if (t0 + 1 < t1)
+                read_pages(t0 + 1);
+            stage_v(t0);
+            if (t0 + 1 < t1)
+                load_k(t0 + 1);
             if (t0 + 2 < t1)
-                cells(t0 + 2);
+                read_pages(t0 + 2);
         }
         __syncthreads();
         for (int t = t0; t < t1; ++t) {
             const int buf = t & 1;
             const bool own = t >= pre_tiles;
             const int j0 = own ? (t - pre_tiles) * kTileKeys : 0;
-            if (wave_rows > 0 && !(own && j0 >= most)) {
-                const uint64_t held = __ballot(key_held[buf][lane] != 0);
-                f32x16 x[2];
-                const uint4 *kl = reinterpret_cast<const uint4 *>(kt[buf]);
+            const bool active = wave_rows > 0 && !(own && j0 >= most);
+            const int left = own ? seen - j0 : INT_MAX;
+            f32x16 x[2];
+            bool masked = false;
+            uint64_t held = 0;
+            if (active) {
+                held = __ballot(key_held[buf][lane] != 0);
+                const uint16_t *kl = kt[buf] + col * KR + half * 8;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         x[b][r] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < KS; ++k)
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
                         x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            as_bf16x8(kl[chunk_at<D>(b * 32 + col, 2 * k + half)]), q[k], x[b], 0, 0, 0);
+                            as_bf16x8(*reinterpret_cast<const uint4 *>(kl + b * 32 * KR + k * 16)), q[k], x[b], 0, 0, 0);
+                // four fragments ahead of the matrix instructions
+                __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 5, 0);
+#pragma unroll
+                for (int k = 0; k < 2 * KS - 4; ++k) {
+                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
                 }
-                const bool masked = held != ~0ull || (own && j0 + kTileKeys > least);
-                const int left = own ? seen - j0 : INT_MAX;
+                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 4, 0);
+                masked = held != ~0ull || (own && j0 + kTileKeys > least);
+            }
+            if (t + 1 < t1) {
+                stage_k(t + 1);
+                load(a.v);
+            }
+            if (active) {
+                // keys 16 i + 4 half + 0..3 and + 8 of column 32 d + col
+                const uint16_t *vl = vt[buf] + (half * 4 + ((lane & 15) >> 2)) * VR + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+                const auto read_v = [&](int i, int d) {
+                    const u32x2 lo = read_tr(vl + i * 16 * VR + d * 32), hi = read_tr(vl + (i * 16 + 8) * VR + d * 32);
+                    return as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1]));
+                };
                 if (masked) {
+                    const uint64_t ok = (held & first_bits64(left)) >> half * 4;
+                    const uint32_t word[2] = {(uint32_t)ok, (uint32_t)(ok >> 32)};
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int key = b * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
-                            x[b][r] = ((held >> key) & 1u) && key < left ? x[b][r] : -INFINITY;
-                        }
+                        for (int r = 0; r < 16; ++r)
+                            x[b][r] = (word[b] >> ((r >> 2) * 8 + (r & 3))) & 1u ? x[b][r] : -INFINITY;
                 }
                 float mx = -INFINITY;
 #pragma unroll
@@ -629,66 +708,54 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
                     for (int r = 0; r < 16; ++r)
                         mx = fmaxf(mx, x[b][r]);
                 mx = fmaxf(mx, __shfl_xor(mx, 32)) * sc;
-                const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.0f : mn;
-                const float keep = exp2_(m - mu);
-                m = mn;
-                float sum = 0.0f;
-                bf16x8 pf[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float e[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        e[r] = exp2_(fmaf(x[i >> 1][(i & 1) * 8 + r], sc, -mu));
-                        sum += e[r];
-                    }
-                    pf[i] = as_bf16x8(make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
-                                                 pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])));
-                }
-                l = fmaf(l, keep, sum);
-                if (__any(keep != 1.0f)) {
+                // the maximum follows only where it grew by more than 2^8: weights
+                // up to 2^8 are as exact, and most tiles need no rescaling
+                if (__any(mx > m + 8.0f)) {
+                    const float mn = fmaxf(m, mx), keep = mn == -INFINITY ? 1.0f : exp2_(m - mn);
+                    m = mn;
+                    l *= keep;
 #pragma unroll
                     for (int d = 0; d < DB; ++d)
                         o[d] *= keep;
                 }
+                const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // keys 16 i + 4 half + 0..3 and + 8
-                    const int r = i * 16 + half * 4 + ((lane & 15) >> 2);
+                    bf16x8 vf[DB];
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const int c = d * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), in = (lane & 1) * 4;
-                        const u32x2 lo = read_tr(vt[buf] + chunk_at<D>(r, c) * 8 + in);
-                        const u32x2 hi = read_tr(vt[buf] + chunk_at<D>(r + 8, c) * 8 + in);
-                        bf16x8 vf = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1])), flags;
-                        if (masked && __any(split_nonfinite(vf, flags))) {
-                            uint4 ones = make_uint4(0, 0, 0, 0);
-                            uint32_t *w = &ones.x;
+                    for (int d = 0; d < DB; ++d)
+                        vf[d] = read_v(i, d);
+                    float e[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int key = i * 16 + (e >> 2) * 8 + half * 4 + (e & 3);
-                                if (((held >> key) & 1u) && key < left)
-                                    w[e >> 1] |= e & 1 ? 0x3F800000u : 0x3F80u;
-                            }
-                            f32x16 bad;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                bad[e] = 0.0f;
-                            bad = __builtin_amdgcn_mfma_f32_32x32x16_bf16(flags, as_bf16x8(ones), bad, 0, 0, 0);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[d][e] = bad[e] > 0.0f ? NAN : o[d][e];
-                        }
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[i], o[d], 0, 0, 0);
+                    for (int r = 0; r < 8; ++r) {
+                        e[r] = exp2_(fmaf(x[i >> 1][(i & 1) * 8 + r], sc, -mu));
+                        l += e[r];
                     }
+                    const bf16x8 pf = as_bf16x8(make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
+                                                           pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])));
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[d], pf, o[d], 0, 0, 0);
+                }
+                if (partial(t) && (any_bad[buf][0] | any_bad[buf][1] | any_bad[buf][2] | any_bad[buf][3])) {
+#pragma unroll 1
+                    for (int key = 0; key < kTileKeys; ++key)
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            const int bits = bad[buf][key][c] >> half * 4;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (((bits >> r) & 1) && key < left)
+                                    o[c >> 2][(c & 3) * 4 + r] = NAN;
+                        }
                 }
             }
             if (t + 1 < t1) {
-                stage(buf ^ 1);
+                stage_v(t + 1);
                 if (t + 2 < t1)
-                    load();
+                    load_k(t + 2);
                 if (t + 3 < t1)
-                    cells(t + 3);
+                    read_pages(t + 3);
             }
             __syncthreads();
         }
