@@ -86,9 +86,10 @@ typedef struct {
  * over).
  * max_new: the largest number of new tokens of one sequence, or 0 where the
  * caller does not know it; a hint for the choice of kernels that no result
- * depends on.  n_seqs, n_groups <= BD_MAX_SEQS; n_tokens < 2^31, and
+ * depends on.  n_seqs <= BD_MAX_SEQS, n_groups <= BD_MAX_GROUPS; n_tokens < 2^31, and
  * n_tokens * n_heads < 2^31 in the calls that take queries. */
 #define BD_MAX_SEQS 4096
+#define BD_MAX_GROUPS 256
 
 typedef struct {
     const int32_t *q_start, *kv_len, *page_table;

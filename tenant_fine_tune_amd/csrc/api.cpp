@@ -537,9 +537,9 @@ bd_status check_batch(const bd_batch *batch)
     const bd_batch &b = *batch;
     if (b.n_tokens < 0 || b.n_tokens > kMaxGrid)
         return fail(BD_ESHAPE, "n_tokens must be in [0, 2^31) (got %lld)", (long long)b.n_tokens);
-    if (b.n_seqs < 0 || b.n_seqs > BD_MAX_SEQS || b.n_groups < 0 || b.n_groups > BD_MAX_SEQS)
-        return fail(BD_ESHAPE, "n_seqs and n_groups must be in [0, %d] (got %d, %d)", BD_MAX_SEQS, b.n_seqs,
-                    b.n_groups);
+    if (b.n_seqs < 0 || b.n_seqs > BD_MAX_SEQS || b.n_groups < 0 || b.n_groups > BD_MAX_GROUPS)
+        return fail(BD_ESHAPE, "n_seqs must be in [0, %d] and n_groups in [0, %d] (got %d, %d)", BD_MAX_SEQS,
+                    BD_MAX_GROUPS, b.n_seqs, b.n_groups);
     if (b.max_new < 0)
         return fail(BD_ESHAPE, "max_new must not be negative (got %d)", b.max_new);
     if (b.n_seqs > 0) {

@@ -140,6 +140,16 @@ __device__ __forceinline__ int64_t scan_block(int64_t v, Scan &sh, int64_t &tota
     return before + x - v;
 }
 
+// Fills the group table.
+__device__ __forceinline__ void fill_groups(const Sched &s, Groups &gr)
+{
+    static_assert(kThreads >= BD_MAX_GROUPS, "a thread per group");
+    if ((int)threadIdx.x < s.p.b.n_groups)
+        fill_group(s, gr, threadIdx.x);
+    if (s.p.b.n_groups)
+        __syncthreads();
+}
+
 // A list of segments whose sizes are laid end to end: thread i sums the
 // sizes of segments [i * per, (i + 1) * per).
 struct Located {
@@ -206,11 +216,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
     __shared__ float2 wave_ml[kWaves][R];
     __shared__ Scan scan;
     __shared__ Located found;
+    __shared__ Groups groups;
 
     const Sched &s = a.s;
     const Paged &p = s.p;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
-    const auto size = [&](int i) { return stream_units(s, i); };
+    fill_groups(s, groups);
+    const auto size = [&](int i) { return stream_units(s, sequence(s, groups, i)); };
     const Listing list(p.b.n_seqs, size, scan);
     const int64_t chunk = stream_chunk(s, list.total), range0 = blockIdx.x * chunk;
     int64_t at = range0;
@@ -219,16 +231,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
         return;
     const Located loc = list.locate(at, &found);
     int seq = loc.first;
-    int64_t base = loc.base, units = stream_units(s, seq);
+    int64_t base = loc.base;
+    Segment g = sequence(s, groups, seq);
     uint16_t *vt = reinterpret_cast<uint16_t *>(lds) + wave * kStreamKeys * VS;
     float *oj = reinterpret_cast<float *>(lds);
 
     while (at < end) {
-        while (base + units <= at) {
+        for (int64_t units; base + (units = stream_units(s, g)) <= at;) {
             base += units;
-            units = stream_units(s, ++seq);
+            g = sequence(s, groups, ++seq);
         }
-        const Segment g = sequence(s, seq);
         const int tiles = key_tiles(g, kStreamKeys), pre_tiles = (int)cdiv(g.pre, kStreamKeys);
         const int64_t row_tiles = stream_row_tiles(s, g), rows = rows_of(s, g);
         const int64_t run = (at - base) / tiles;
@@ -483,21 +495,23 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
     __shared__ uint32_t any_bad[2][kWaves];
     __shared__ Scan scan;
     __shared__ Located found;
+    __shared__ Groups groups;
 
     const Sched &s = a.s;
     const Paged &p = s.p;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
     const int n_seg = p.b.n_seqs + p.b.n_groups;
     int64_t depth;
+    fill_groups(s, groups);
     {
         const auto work = [&](int i) {
-            const Segment g = tiled_segment(s, i);
+            const Segment g = tiled_segment(s, groups, i);
             return g.ntok ? tiled_work(s, g) : 0;
         };
         const Listing<decltype(work)> all(n_seg, work, scan);
         depth = tiled_depth(s, all.total);
     }
-    const auto size = [&](int i) { return tiled_items(s, tiled_segment(s, i), depth); };
+    const auto size = [&](int i) { return tiled_items(s, tiled_segment(s, groups, i), depth); };
     const Listing<decltype(size)> list(n_seg, size, scan);
 
     for (int64_t item = blockIdx.x; item < list.total; item += gridDim.x) {
@@ -506,7 +520,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
         int64_t base = loc.base;
         Segment g;
         for (;; ++seg) {
-            g = tiled_segment(s, seg);
+            g = tiled_segment(s, groups, seg);
             const int64_t n = tiled_items(s, g, depth);
             if (item < base + n)
                 break;
@@ -799,6 +813,7 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
     constexpr int N = D / 64;
     __shared__ Scan scan;
     __shared__ Located found;
+    __shared__ Groups groups;
     const Sched &s = a.s;
     const Paged &p = s.p;
     const int64_t tok = blockIdx.x;
@@ -812,13 +827,14 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
     Segment g;
     int64_t units0 = 0, chunk = 1;
     if (seq >= 0) {
-        g = sequence(s, seq);
+        fill_groups(s, groups);
+        g = sequence(s, groups, seq);
         by_stream = streamed(s, g);
         const int64_t none = 0;
         if (s.tiled && (g.shared || (!by_stream && s.splits > 1))) {
             const int n_seg = p.b.n_seqs + p.b.n_groups;
             const auto work = [&](int i) {
-                const Segment q = tiled_segment(s, i);
+                const Segment q = tiled_segment(s, groups, i);
                 return q.ntok ? tiled_work(s, q) : none;
             };
             const Listing<decltype(work)> all(n_seg, work, scan);
@@ -826,14 +842,14 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
             if (!by_stream)
                 own_parts = tiled_splits(s, g, depth);
             if (g.shared)
-                prefix_parts = tiled_splits(s, prefix(s, g.group), depth);
+                prefix_parts = tiled_splits(s, prefix(s, groups, g.group), depth);
         } else if (!by_stream) {
             own_parts = 1;
         }
         if (!by_stream && own_parts == 1 && !g.shared)
             return;
         if (by_stream) {
-            const auto size = [&](int i) { return stream_units(s, i); };
+            const auto size = [&](int i) { return stream_units(s, sequence(s, groups, i)); };
             const Listing<decltype(size)> list(p.b.n_seqs, size, scan);
             chunk = stream_chunk(s, list.total);
             units0 = list.begin(seq, size, &found);

@@ -49,38 +49,40 @@ struct Segment {
 
 BD_HD int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-BD_HD bool group_shared(const Sched &s, int g)
+// Group g's entry of `gr` (and with the last group the end of the list).
+BD_HD void fill_group(const Sched &s, Groups &gr, int g)
 {
     const int a = group_begin(s.p, g), b = group_begin(s.p, g + 1);
-    if (!s.tiled || b - a < 2 || prefix_keys(s.p, g) == 0)
-        return false;
+    gr.begin[g] = a;
+    if (g == s.p.b.n_groups - 1)
+        gr.begin[g + 1] = b;
+    gr.prefix[g] = prefix_keys(s.p, g);
     const int64_t toks = (int64_t)seq_begin(s.p, b) - seq_begin(s.p, a);
-    return toks > 0 && toks <= (int64_t)kSharedNew * (b - a);
+    gr.shared[g] = s.tiled && b - a >= 2 && gr.prefix[g] > 0 && toks > 0 && toks <= (int64_t)kSharedNew * (b - a);
 }
 
-BD_HD Segment sequence(const Sched &s, int i)
+BD_HD Segment sequence(const Sched &s, const Groups &gr, int i)
 {
     Segment g;
     g.tok0 = seq_begin(s.p, i);
     const int n = seq_begin(s.p, i + 1) - g.tok0;
     g.ntok = n < 0 ? 0 : n;
     g.own = own_keys(s.p, i);
-    g.group = s.p.b.n_groups ? group_of(s.p, i) : -1;
-    g.shared = g.group >= 0 && group_shared(s, g.group);
-    g.pre = g.group >= 0 && !g.shared ? prefix_keys(s.p, g.group) : 0;
+    g.group = s.p.b.n_groups ? group_of(s.p, gr, i) : -1;
+    g.shared = g.group >= 0 && gr.shared[g.group];
+    g.pre = g.group >= 0 && !g.shared ? gr.prefix[g.group] : 0;
     return g;
 }
 
 // The shared prefix of group g as a segment of its own (no tokens: not shared).
-BD_HD Segment prefix(const Sched &s, int g)
+BD_HD Segment prefix(const Sched &s, const Groups &gr, int g)
 {
     Segment q;
-    const int a = group_begin(s.p, g), b = group_begin(s.p, g + 1);
-    q.shared = group_shared(s, g);
+    q.shared = gr.shared[g];
     q.group = g;
-    q.tok0 = q.shared ? seq_begin(s.p, a) : 0;
-    q.ntok = q.shared ? seq_begin(s.p, b) - q.tok0 : 0;
-    q.pre = q.shared ? prefix_keys(s.p, g) : 0;
+    q.tok0 = q.shared ? seq_begin(s.p, gr.begin[g]) : 0;
+    q.ntok = q.shared ? seq_begin(s.p, gr.begin[g + 1]) - q.tok0 : 0;
+    q.pre = q.shared ? gr.prefix[g] : 0;
     q.own = 0;
     return q;
 }
@@ -98,9 +100,8 @@ BD_HD int own_seen(const Segment &g, int i)
 
 // ------------------------------------------------------------ streaming kernel
 BD_HD int64_t stream_row_tiles(const Sched &s, const Segment &g) { return cdiv(rows_of(s, g), s.stream_rows); }
-BD_HD int64_t stream_units(const Sched &s, int i)
+BD_HD int64_t stream_units(const Sched &s, const Segment &g)
 {
-    const Segment g = sequence(s, i);
     return g.ntok && streamed(s, g) ? s.p.n_kv * stream_row_tiles(s, g) * key_tiles(g, kStreamKeys) : 0;
 }
 // Units of a workgroup, of `total` in all.
@@ -112,11 +113,11 @@ BD_HD int64_t stream_chunk(const Sched &s, int64_t total)
 
 // ---------------------------------------------------------------- tiled kernel
 // Segments [0, n_seqs) are sequences, the next n_groups shared prefixes.
-BD_HD Segment tiled_segment(const Sched &s, int i)
+BD_HD Segment tiled_segment(const Sched &s, const Groups &gr, int i)
 {
     if (i >= s.p.b.n_seqs)
-        return prefix(s, i - s.p.b.n_seqs);
-    Segment g = sequence(s, i);
+        return prefix(s, gr, i - s.p.b.n_seqs);
+    Segment g = sequence(s, gr, i);
     if (streamed(s, g))
         g.ntok = 0;
     return g;

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void append_tokens(AppendArgs a)
     if (placed) {
         const int at = own_keys(p, s) - (seq_begin(p, s + 1) - (int)t);
         placed = at >= 0;
-        const int g = group_of(p, s);
+        const int g = group_around(p, s);
         if (placed) {
             cell = cell_of(p, p.b.page_table + (int64_t)s * p.b.max_pages, 0, at);
             const double pos = (double)at + (g >= 0 ? prefix_keys(p, g) : 0);

@@ -35,19 +35,26 @@ BD_HD int prefix_keys(const Paged &p, int g) { return clampi(p.b.prefix_len[g], 
 
 BD_HD int group_begin(const Paged &p, int g) { return clampi(p.b.group_start[g], 0, p.b.n_seqs); }
 
+// The groups of a batch, held in LDS: what a sequence has to know of its own.
+struct Groups {
+    int begin[BD_MAX_GROUPS + 1];     // first sequence
+    int prefix[BD_MAX_GROUPS];        // keys
+    uint8_t shared[BD_MAX_GROUPS];    // see attention_schedule.h
+};
+
 // The group of sequence s, or -1: the number of groups that end at or before
 // s, where the starts do not decrease.
-BD_HD int group_of(const Paged &p, int s)
+BD_HD int group_of(const Paged &p, const Groups &gr, int s)
 {
     int lo = 0, hi = p.b.n_groups;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (group_begin(p, mid + 1) <= s)
+        if (gr.begin[mid + 1] <= s)
             lo = mid + 1;
         else
             hi = mid;
     }
-    return lo < p.b.n_groups && group_begin(p, lo) <= s && s < group_begin(p, lo + 1) ? lo : -1;
+    return lo < p.b.n_groups && gr.begin[lo] <= s && s < gr.begin[lo + 1] ? lo : -1;
 }
 
 // The cell (in units of head_dim numbers) of one head's key j of a page list,
@@ -71,6 +78,19 @@ __device__ __forceinline__ int seq_of(const Paged &p, int64_t t)
         s += __syncthreads_count(j < p.b.n_seqs && seq_begin(p, j + 1) <= t);
     }
     return s < p.b.n_seqs && seq_begin(p, s) <= t && t < seq_begin(p, s + 1) ? s : -1;
+}
+
+// The group of sequence s, or -1, found by the whole workgroup without a table.
+__device__ __forceinline__ int group_around(const Paged &p, int s)
+{
+    if (!p.b.n_groups)
+        return -1;
+    int g = 0;
+    for (int i = 0; i < p.b.n_groups; i += blockDim.x) {
+        const int j = i + threadIdx.x;
+        g += __syncthreads_count(j < p.b.n_groups && group_begin(p, j + 1) <= s);
+    }
+    return g < p.b.n_groups && group_begin(p, g) <= s && s < group_begin(p, g + 1) ? g : -1;
 }
 
 }  // namespace bd

@@ -94,6 +94,9 @@ int main()
         Case c = make(r, current % 2 == 0);
         const Sched &s = c.s;
         const Paged &p = s.p;
+        Groups gr;
+        for (int g = 0; g < p.b.n_groups; ++g)
+            fill_group(s, gr, g);
         const int64_t T = p.b.n_tokens, H = s.n_heads;
         typedef std::pair<int64_t, int64_t> Row;                       // token, head
         std::map<Row, std::map<int64_t, int>> weighed;                  // key: place, or -1 - place of a prefix
@@ -127,16 +130,16 @@ int main()
         int64_t total = 0;
         std::vector<int64_t> begin;
         for (int i = 0; i < p.b.n_seqs; ++i)
-            begin.push_back(total), total += stream_units(s, i);
+            begin.push_back(total), total += stream_units(s, sequence(s, gr, i));
         const int64_t chunk = stream_chunk(s, total);
         for (int64_t w = 0; w < s.stream_wgs; ++w) {
             int64_t at = w * chunk, end = std::min(total, at + chunk);
             int seq = 0;
             while (at < end) {
-                while (begin[seq] + stream_units(s, seq) <= at)
+                while (begin[seq] + stream_units(s, sequence(s, gr, seq)) <= at)
                     ++seq;
                 EXPECT(seq < p.b.n_seqs);
-                const Segment g = sequence(s, seq);
+                const Segment g = sequence(s, gr, seq);
                 const int tiles = key_tiles(g, kStreamKeys);
                 const int64_t run = (at - begin[seq]) / tiles, rt = stream_row_tiles(s, g);
                 const int t0 = (int)((at - begin[seq]) % tiles), t1 = (int)std::min<int64_t>(tiles, t0 + end - at);
@@ -164,13 +167,13 @@ int main()
         int64_t work = 0, depth;
         const int n_seg = p.b.n_seqs + p.b.n_groups;
         for (int i = 0; i < n_seg; ++i) {
-            const Segment g = tiled_segment(s, i);
+            const Segment g = tiled_segment(s, gr, i);
             work += g.ntok ? tiled_work(s, g) : 0;
         }
         depth = tiled_depth(s, work);
         EXPECT(s.tiled || work == 0);
         for (int seg = 0; seg < n_seg; ++seg) {
-            const Segment g = tiled_segment(s, seg);
+            const Segment g = tiled_segment(s, gr, seg);
             const int64_t items = tiled_items(s, g, depth);
             for (int64_t idx = 0; idx < items; ++idx) {
                 const int splits = tiled_splits(s, g, depth), head = (int)(idx % p.n_kv);
@@ -208,7 +211,7 @@ int main()
                 bool done = false;
                 const int64_t out = tok * H + h;
                 if (seq >= 0) {
-                    const Segment g = sequence(s, seq);
+                    const Segment g = sequence(s, gr, seq);
                     if (streamed(s, g)) {
                         const int tiles = key_tiles(g, kStreamKeys), head = h / s.group;
                         const int64_t row = (tok - g.tok0) * s.group + h % s.group;
@@ -232,7 +235,7 @@ int main()
                                 reads.push_back(slots + i * plane + out);
                     }
                     if (g.shared)
-                        for (int i = 0; i < tiled_splits(s, prefix(s, g.group), depth); ++i)
+                        for (int i = 0; i < tiled_splits(s, prefix(s, gr, g.group), depth); ++i)
                             reads.push_back(slots + (s.splits + i) * plane + out);
                 }
                 for (int64_t pr : reads)
@@ -247,7 +250,7 @@ int main()
                     const int own = own_keys(p, seq), at = own - (seq_begin(p, seq + 1) - (int)tok);
                     for (int j = 0; j <= at; ++j)
                         want[j] = 1;
-                    const int g = group_of(p, seq);
+                    const int g = group_of(p, gr, seq);
                     for (int j = 0; g >= 0 && j < prefix_keys(p, g); ++j)
                         want[-1 - (int64_t)j] = 1;
                 }

@@ -63,7 +63,7 @@ BAD_CACHE = [
 ]
 BAD_BATCH = [
     (dict(n_tokens=-1), "ESHAPE"), (dict(n_tokens=2 ** 31), "ESHAPE"), (dict(n_seqs=-1), "ESHAPE"),
-    (dict(n_seqs=4097), "ESHAPE"), (dict(n_groups=-1), "ESHAPE"), (dict(n_groups=4097), "ESHAPE"),
+    (dict(n_seqs=4097), "ESHAPE"), (dict(n_groups=-1), "ESHAPE"), (dict(n_groups=257), "ESHAPE"),
     (dict(max_new=-1), "ESHAPE"), (dict(max_pages=0), "ESHAPE"), (dict(q_start=None), "EINVAL"),
     (dict(kv_len=None), "EINVAL"), (dict(page_table=None), "EINVAL"), (dict(kv_len=ODD), "EALIGN"),
     (dict(n_groups=1, max_prefix_pages=0, group_start=FAKE, prefix_len=FAKE, prefix_table=FAKE), "ESHAPE"),
