@@ -6,7 +6,7 @@
 //   m' = max(m, s);  l = l 2^(m - m') + sum 2^(s - m');  o likewise with v,
 // s = log2(e) scale q.k, in fp32; the weights 2^(s - m') enter the product
 // with v rounded to bf16 (half a step, 2^-8 relative), as the matrix
-// instructions take them, while l sums them unrounded.  Keys that a row does
+// instructions take them, and l sums the rounded ones in fp32.  Keys that a row does
 // not see have s = -inf.  States over parts of the keys are joined by the
 // same formula (attention_join).
 //
@@ -38,6 +38,7 @@ struct AttnArgs {
     const uint8_t *k, *v;
     const float *k_scale, *v_scale;
     uint16_t *out;
+    int64_t *cut;       // what the join has to know: key tiles of a split, units of a workgroup, first unit of each sequence
     float *part_o;      // partial states: [rows][head_dim], slots first, then planes
     float2 *part_ml;    // their m and l
     int64_t q_stride;
@@ -48,6 +49,20 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ bf16x8 as_bf16x8(uint4 w) { return __builtin_bit_cast(bf16x8, w); }
+
+// Eight weights as the bf16 operand of the second product; l sums what the
+// product takes, the rounded weights, so that they add up to one.
+__device__ __forceinline__ bf16x8 weights(const float *e, float &l)
+{
+    const uint4 w = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                               pack_bf16x2(e[6], e[7]));
+    constexpr uint32_t ones = 0x3F803F80u;
+    l = dot2(w.x, ones, l);
+    l = dot2(w.y, ones, l);
+    l = dot2(w.z, ones, l);
+    l = dot2(w.w, ones, l);
+    return as_bf16x8(w);
+}
 
 // Four e4m3 numbers as four bf16 (exact).
 __device__ __forceinline__ u32x2 e4m3_to_bf16(uint32_t w)
@@ -140,6 +155,28 @@ __device__ __forceinline__ int64_t scan_block(int64_t v, Scan &sh, int64_t &tota
     return before + x - v;
 }
 
+// Sums of two values over the workgroup's threads.
+__device__ __forceinline__ void sum_block(int64_t &x, int64_t &y, Scan &sx, Scan &sy)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        x += __shfl_xor(x, o), y += __shfl_xor(y, o);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        sx.wave[threadIdx.x >> 6] = x, sy.wave[threadIdx.x >> 6] = y;
+    __syncthreads();
+    x = y = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+        x += sx.wave[i], y += sy.wave[i];
+}
+
+// a / b for a >= 0, b > 0: nearly always within 32 bits, where it is far cheaper.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Fills the group table.
 __device__ __forceinline__ void fill_groups(const Sched &s, Groups &gr)
 {
@@ -178,18 +215,6 @@ struct Listing {
         __syncthreads();
         return *sh;
     }
-    // where segment i begins
-    __device__ __forceinline__ int64_t begin(int i, const Size &size, Located *sh) const
-    {
-        __syncthreads();
-        if ((int)threadIdx.x == i / per)
-            sh->base = before;
-        __syncthreads();
-        int64_t b = sh->base;
-        for (int j = i / per * per; j < i; ++j)
-            b += size(j);
-        return b;
-    }
 };
 
 // ------------------------------------------------------------ few rows: stream
@@ -224,9 +249,18 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
     fill_groups(s, groups);
     const auto size = [&](int i) { return stream_units(s, sequence(s, groups, i)); };
     const Listing list(p.b.n_seqs, size, scan);
-    const int64_t chunk = stream_chunk(s, list.total), range0 = blockIdx.x * chunk;
-    int64_t at = range0;
+    const int64_t chunk = stream_chunk(s, list.total);
+    int64_t at = blockIdx.x * chunk;
     const int64_t end = min(list.total, at + chunk);
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0)
+            a.cut[1] = chunk;
+        int64_t b = list.before;
+        for (int i = threadIdx.x * list.per; i < min(list.n, (int)(threadIdx.x + 1) * list.per); ++i) {
+            a.cut[2 + i] = b;
+            b += list.per > 1 ? size(i) : 0;
+        }
+    }
     if (at >= end)
         return;
     const Located loc = list.locate(at, &found);
@@ -243,9 +277,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
         }
         const int tiles = key_tiles(g, kStreamKeys), pre_tiles = (int)cdiv(g.pre, kStreamKeys);
         const int64_t row_tiles = stream_row_tiles(s, g), rows = rows_of(s, g);
-        const int64_t run = (at - base) / tiles;
-        const int t0 = (int)((at - base) - run * tiles), t1 = (int)min((int64_t)tiles, t0 + (end - at));
-        const int head = (int)(run / row_tiles);
+        const int len = stream_run(g);
+        const int64_t run = quotient(at - base, len);
+        const int from = (int)((at - base) - run * len), to = (int)min((int64_t)len, from + (end - at));
+        const int t0 = max(from - kRunCost, 0), t1 = to - kRunCost;
+        at += to - from;
+        if (t0 >= t1)
+            continue;
+        const int head = (int)quotient(run, row_tiles);
         const int row0 = (int)(run - head * row_tiles) * R;
         const int32_t *own_table = p.b.page_table + (int64_t)seq * p.b.max_pages;
         const int32_t *pre_table = g.pre ? p.b.prefix_table + (int64_t)g.group * p.b.max_prefix_pages : own_table;
@@ -379,15 +418,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
                 const float mn = fmaxf(m[n], mx), mu = mn == -INFINITY ? 0.0f : mn;
                 const float keep = exp2_(m[n] - mu);
                 m[n] = mn;
-                float e[8], sum = 0.0f;
+                float e[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 8; ++i)
                     e[i] = exp2_(fmaf(x[n][i >> 2][i & 3], sc, -mu));
-                    sum += e[i];
-                }
-                l[n] = fmaf(l[n], keep, sum);
-                pf[n] = as_bf16x8(make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                                             pack_bf16x2(e[6], e[7])));
+                l[n] *= keep;
+                pf[n] = weights(e, l[n]);
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
                     o[n][d] *= keep;
@@ -470,7 +506,6 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
             }
         }
         __syncthreads();
-        at += t1 - t0;
     }
 }
 
@@ -485,15 +520,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
 {
     constexpr int KS = D / 16, DB = D / 32;
     constexpr int ES = E4M3 ? 1 : 2;
-    constexpr int LPR = D * ES / 16;                          // threads that load a row
-    constexpr int NL = kTileKeys * LPR / kThreads;            // loads of a thread, K and V each
-    constexpr int RPI = kThreads / LPR;
-    static_assert(NL >= 1, "a tile is at least one load of every thread");
+    constexpr int NL = D * ES / 64;   // loads of a thread, K and V each: four threads a key, 64 bytes a load
+    static_assert(kThreads == 4 * kTileKeys, "four threads a key");
     constexpr int KR = Stride<D>::k, VR = Stride<D>::v;
     __shared__ __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * KR], vt[2][kTileKeys * VR];
     __shared__ uint8_t key_held[2][kTileKeys], bad[2][kTileKeys][D / 8];
     __shared__ uint32_t any_bad[2][kWaves];
-    __shared__ Scan scan;
+    __shared__ Scan scan, scan2;
     __shared__ Located found;
     __shared__ Groups groups;
 
@@ -501,16 +534,28 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
     const Paged &p = s.p;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
     const int n_seg = p.b.n_seqs + p.b.n_groups;
-    int64_t depth;
+    int64_t depth = INT_MAX;
     fill_groups(s, groups);
-    {
-        const auto work = [&](int i) {
+    if (s.splits > 1) {
+        int64_t work = 0, items = 0;
+        for (int i = threadIdx.x; i < n_seg; i += kThreads) {
             const Segment g = tiled_segment(s, groups, i);
-            return g.ntok ? tiled_work(s, g) : 0;
-        };
-        const Listing<decltype(work)> all(n_seg, work, scan);
-        depth = tiled_depth(s, all.total);
+            if (g.ntok) {
+                work += tiled_work(s, g);
+                items += p.n_kv * tiled_row_tiles(s, g);
+            }
+        }
+        sum_block(work, items, scan, scan2);
+        // lane k - 1 tries k
+        float best = lane < s.splits && items > 0 ? tiled_time(items, work, lane + 1) : INFINITY;
+        const float mine = best;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1)
+            best = fminf(best, __shfl_xor(best, o));
+        depth = tiled_depth(items, work, __ffsll(__ballot(mine == best)));
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        a.cut[0] = depth;
     const auto size = [&](int i) { return tiled_items(s, tiled_segment(s, groups, i), depth); };
     const Listing<decltype(size)> list(n_seg, size, scan);
 
@@ -529,9 +574,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
         // heads fastest, then splits, then row tiles from the last (the longest) to the first
         const int64_t idx = item - base;
         const int splits = tiled_splits(s, g, depth);
-        const int head = (int)(idx % p.n_kv), split = (int)(idx / p.n_kv % splits);
+        const int64_t idx2 = quotient(idx, p.n_kv), idx3 = quotient(idx2, splits);
+        const int head = (int)(idx - idx2 * p.n_kv), split = (int)(idx2 - idx3 * splits);
         const int64_t rows = rows_of(s, g);
-        const int row0 = (int)(tiled_row_tiles(s, g) - 1 - idx / p.n_kv / splits) * kTileRows;
+        const int row0 = (int)(tiled_row_tiles(s, g) - 1 - idx3) * kTileRows;
         const int rows_here = (int)min((int64_t)kTileRows, rows - row0);
         const int pre_tiles = (int)cdiv(g.pre, kTileKeys);
         const bool is_prefix = seg >= p.b.n_seqs;
@@ -570,58 +616,54 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
         // One set of registers carries K of the next tile until the scores of
         // this one are done, then its V.  A key without a cell reads cell 0: its
         // score is masked, its value cleared.
-        int page[NL], cell[NL];
+        int page = 0, cell = -1;
         uint4 in[NL];
-        const auto tile_keys = [&](int t, int &j0) {
+        const uint8_t *src = nullptr;
+        // Four threads a key, so a key's cell and address are formed once.  The
+        // 16 keys of a wave are dealt so that 16 neighbouring threads, four keys,
+        // write to different banks under both row strides.
+        const int part = threadIdx.x & 3, k4 = (lane >> 2) & 3;
+        const int ldr = wave * 16 + k4 * 4 + ((k4 + (lane >> 4)) & 3);
+        const auto read_page = [&](int t) {
             const bool own = t >= pre_tiles;
-            j0 = (own ? t - pre_tiles : t) * kTileKeys + threadIdx.x / LPR;
-            return own ? g.own : g.pre;
+            const int j = (own ? t - pre_tiles : t) * kTileKeys + ldr;
+            page = (own ? own_table : pre_table)[min(j, (own ? g.own : g.pre) - 1) >> p.page_shift];
         };
-        const auto read_pages = [&](int t) {
-            int j0;
-            const int n = tile_keys(t, j0);
-            const int32_t *table = t >= pre_tiles ? own_table : pre_table;
+        const auto load = [&](const uint8_t *from) {
 #pragma unroll
             for (int i = 0; i < NL; ++i)
-                page[i] = table[min(j0 + i * RPI, n - 1) >> p.page_shift];
-        };
-        const auto load = [&](const uint8_t *cache) {
-#pragma unroll
-            for (int i = 0; i < NL; ++i)
-                in[i] = *reinterpret_cast<const uint4 *>(cache + (uint64_t)max(cell[i], 0) * (D * ES) +
-                                                         threadIdx.x % LPR * 16);
+                in[i] = *reinterpret_cast<const uint4 *>(from + i * 64);
         };
         const auto load_k = [&](int t) {
-            int j0;
-            const int n = tile_keys(t, j0);
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int j = j0 + i * RPI;
-                cell[i] = j < n && (unsigned)page[i] < (unsigned)p.n_pages
-                              ? ((page[i] * p.n_kv + head) << p.page_shift) + (j & ((1 << p.page_shift) - 1)) : -1;
-            }
-            load(a.k);
+            const bool own = t >= pre_tiles;
+            const int j = (own ? t - pre_tiles : t) * kTileKeys + ldr;
+            cell = j < (own ? g.own : g.pre) && (unsigned)page < (unsigned)p.n_pages
+                       ? ((page * p.n_kv + head) << p.page_shift) + (j & ((1 << p.page_shift) - 1)) : -1;
+            const uint64_t off = (uint64_t)max(cell, 0) * (D * ES) + part * 16;
+            src = a.v + off;
+            load(a.k + off);
         };
         // some row of the workgroup does not see all of tile t's keys that others see
         const auto partial = [&](int t) { return t >= pre_tiles && (t - pre_tiles + 1) * kTileKeys > least_all; };
-        const int ldr = threadIdx.x / LPR, ldc = threadIdx.x % LPR * (E4M3 ? 2 : 1);
+        const int ldc = part * (E4M3 ? 2 : 1);                     // first of a load's 8-column pieces
+        constexpr int PIECES = E4M3 ? 2 : 1, STEP = 4 * PIECES;
         const auto stage_k = [&](int t) {
-            uint16_t *dst = kt[t & 1] + ldr * KR + ldc * 8;
+            uint4 *dst = reinterpret_cast<uint4 *>(kt[t & 1] + ldr * KR + ldc * 8);
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                uint4 *w = reinterpret_cast<uint4 *>(dst + i * RPI * KR);
-                if (E4M3)
-                    w[0] = e4m3x8_to_bf16(in[i].x, in[i].y), w[1] = e4m3x8_to_bf16(in[i].z, in[i].w);
-                else
-                    w[0] = in[i];
-                if (ldc == 0)
-                    key_held[t & 1][ldr + i * RPI] = cell[i] >= 0;
-            }
+            for (int i = 0; i < NL; ++i)
+                if (E4M3) {
+                    dst[i * STEP] = e4m3x8_to_bf16(in[i].x, in[i].y);
+                    dst[i * STEP + 1] = e4m3x8_to_bf16(in[i].z, in[i].w);
+                } else {
+                    dst[i * STEP] = in[i];
+                }
+            if (part == 0)
+                key_held[t & 1][ldr] = cell >= 0;
         };
         const auto stage_v = [&](int t) {
             const int buf = t & 1;
-            uint16_t *dst = vt[buf] + ldr * VR + ldc * 8;
-            const bool check = partial(t);
+            uint4 *dst = reinterpret_cast<uint4 *>(vt[buf] + ldr * VR + ldc * 8);
+            const bool check = partial(t), hole = __any(cell < 0);
             uint32_t found_bad = 0;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
@@ -629,15 +671,15 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
                 if (E4M3)
                     v[0] = e4m3x8_to_bf16(in[i].x, in[i].y), v[1] = e4m3x8_to_bf16(in[i].z, in[i].w);
 #pragma unroll
-                for (int e = 0; e < (E4M3 ? 2 : 1); ++e) {
-                    if (cell[i] < 0)
+                for (int e = 0; e < PIECES; ++e) {
+                    if (hole && cell < 0)
                         v[e] = make_uint4(0, 0, 0, 0);
                     if (check) {
                         const uint32_t bits = take_nonfinite(v[e]);
-                        bad[buf][ldr + i * RPI][ldc + e] = (uint8_t)bits;
+                        bad[buf][ldr][ldc + i * STEP + e] = (uint8_t)bits;
                         found_bad |= bits;
                     }
-                    reinterpret_cast<uint4 *>(dst + i * RPI * VR)[e] = v[e];
+                    dst[i * STEP + e] = v[e];
                 }
             }
             if (check) {
@@ -649,17 +691,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
         // q has to be there before the loop: its wait inside would be one for all loads in flight
         wait_vmcnt<0>();
         if (t0 < t1) {
-            read_pages(t0);
+            read_page(t0);
             load_k(t0);
             stage_k(t0);
-            load(a.v);
+            load(src);
             if (t0 + 1 < t1)
-                read_pages(t0 + 1);
+                read_page(t0 + 1);
             stage_v(t0);
             if (t0 + 1 < t1)
                 load_k(t0 + 1);
             if (t0 + 2 < t1)
-                read_pages(t0 + 2);
+                read_page(t0 + 2);
         }
         __syncthreads();
         for (int t = t0; t < t1; ++t) {
@@ -697,7 +739,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
             }
             if (t + 1 < t1) {
                 stage_k(t + 1);
-                load(a.v);
+                load(src);
             }
             if (active) {
                 // keys 16 i + 4 half + 0..3 and + 8 of column 32 d + col
@@ -741,12 +783,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
                         vf[d] = read_v(i, d);
                     float e[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
+                    for (int r = 0; r < 8; ++r)
                         e[r] = exp2_(fmaf(x[i >> 1][(i & 1) * 8 + r], sc, -mu));
-                        l += e[r];
-                    }
-                    const bf16x8 pf = as_bf16x8(make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
-                                                           pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])));
+                    const bf16x8 pf = weights(e, l);
 #pragma unroll
                     for (int d = 0; d < DB; ++d)
                         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[d], pf, o[d], 0, 0, 0);
@@ -769,7 +808,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
                 if (t + 2 < t1)
                     load_k(t + 2);
                 if (t + 3 < t1)
-                    read_pages(t + 3);
+                    read_page(t + 3);
             }
             __syncthreads();
         }
@@ -811,8 +850,6 @@ template <int D>
 __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
 {
     constexpr int N = D / 64;
-    __shared__ Scan scan;
-    __shared__ Located found;
     __shared__ Groups groups;
     const Sched &s = a.s;
     const Paged &p = s.p;
@@ -830,30 +867,16 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
         fill_groups(s, groups);
         g = sequence(s, groups, seq);
         by_stream = streamed(s, g);
-        const int64_t none = 0;
-        if (s.tiled && (g.shared || (!by_stream && s.splits > 1))) {
-            const int n_seg = p.b.n_seqs + p.b.n_groups;
-            const auto work = [&](int i) {
-                const Segment q = tiled_segment(s, groups, i);
-                return q.ntok ? tiled_work(s, q) : none;
-            };
-            const Listing<decltype(work)> all(n_seg, work, scan);
-            const int64_t depth = tiled_depth(s, all.total);
-            if (!by_stream)
-                own_parts = tiled_splits(s, g, depth);
-            if (g.shared)
-                prefix_parts = tiled_splits(s, prefix(s, groups, g.group), depth);
-        } else if (!by_stream) {
-            own_parts = 1;
+        const int64_t depth = s.tiled ? a.cut[0] : 1;
+        chunk = a.cut[1];
+        units0 = a.cut[2 + seq];
+        if (!by_stream) {
+            own_parts = tiled_splits(s, g, depth);
+            if (own_parts == 1 && !g.shared)
+                return;
         }
-        if (!by_stream && own_parts == 1 && !g.shared)
-            return;
-        if (by_stream) {
-            const auto size = [&](int i) { return stream_units(s, sequence(s, groups, i)); };
-            const Listing<decltype(size)> list(p.b.n_seqs, size, scan);
-            chunk = stream_chunk(s, list.total);
-            units0 = list.begin(seq, size, &found);
-        }
+        if (g.shared)
+            prefix_parts = tiled_splits(s, prefix(s, groups, g.group), depth);
     }
     const int tiles = seq >= 0 ? key_tiles(g, kStreamKeys) : 0;
     for (int h = blockIdx.y * kWaves + wave; h < s.n_heads; h += gridDim.y * kWaves) {
@@ -864,11 +887,12 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
         if (by_stream && tiles) {
             const int head = h / s.group;
             const int64_t row = (tok - g.tok0) * s.group + h - head * s.group;
-            const int64_t u0 = units0 + (head * stream_row_tiles(s, g) + row / s.stream_rows) * tiles;
-            first_wg = u0 / chunk;
-            parts = (int)((u0 + tiles - 1) / chunk - first_wg) + 1;
+            const int64_t u0 = units0 + kRunCost +
+                               (head * stream_row_tiles(s, g) + (int)row / s.stream_rows) * stream_run(g);
+            first_wg = quotient(u0, chunk);
+            parts = (int)(quotient(u0 + tiles - 1, chunk) - first_wg) + 1;
             slotted = parts > 1;
-            row_in = row % s.stream_rows;
+            row_in = (int)row % s.stream_rows;
             if (!slotted && !g.shared)
                 continue;
         }
@@ -935,6 +959,8 @@ struct Plan {
     int64_t tiled_grid, rows;     // rows of partial states
 };
 
+size_t cut_bytes(const bd_batch &b) { return (size_t)(2 + b.n_seqs + 1) / 2 * 16; }
+
 Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
 {
     Plan pl;
@@ -948,15 +974,17 @@ Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
     s.tiled = b.n_groups > 0 || most > 32;
     s.few = s.tiled ? 32 : INT_MAX;
     s.stream_wgs = 512;
-    // enough splits that row tiles x key heads x splits fill the chip one and a half times
+    // enough splits that row tiles x key heads x splits fill the chip twice
     const int64_t tiles = cdiv(T * s.group, kTileRows) * c.n_kv_heads;
-    const int64_t want = cdiv(768, tiles);
+    const int64_t want = cdiv(2 * kTiledSlots, tiles);
     s.splits = s.tiled ? (int32_t)(want < 1 ? 1 : want > 64 ? 64 : want) : 1;
     const int64_t planes = b.n_groups > 0 ? 2 * s.splits : s.splits > 1 ? s.splits : 0;
     pl.rows = 2 * (int64_t)s.stream_wgs * s.stream_rows + planes * T * n_heads;
-    const int64_t segs = (b.n_seqs < T ? b.n_seqs : T) + (b.n_groups < T ? b.n_groups : T);
-    const int64_t most_items = (2 * (T * s.group / kTileRows) + segs) * c.n_kv_heads + kTiledSlots;
-    pl.tiled_grid = most_items < 8192 ? most_items : 8192;
+    // a workgroup per item; where items are split they are few, and the bound is loose
+    const int64_t full = T * s.group / kTileRows;
+    const int64_t row_tiles = full + (b.n_seqs < T ? b.n_seqs : T) + (b.n_groups > 0 ? full + b.n_groups : 0);
+    const int64_t items = row_tiles * c.n_kv_heads * s.splits, cap = s.splits > 1 ? 2 * kTiledSlots : INT_MAX;
+    pl.tiled_grid = items < 1 ? 1 : items < cap ? items : cap;
     return pl;
 }
 
@@ -971,7 +999,7 @@ void start(const AttnArgs &a, const Plan &pl, hipStream_t st)
     else
         attention_stream<D, E4M3, 2><<<dim3(s.stream_wgs), kThreads, 0, st>>>(a);
     const int64_t T = s.p.b.n_tokens, waves = (s.n_heads + kWaves - 1) / kWaves;
-    const int64_t y = 1024 / T;
+    const int64_t y = 8192 / T;
     attention_join<D><<<dim3((unsigned)T, (unsigned)(y < 1 ? 1 : y > waves ? waves : y)), kThreads, 0, st>>>(a);
 }
 
@@ -981,7 +1009,7 @@ size_t attention_workspace_bytes(int32_t n_heads, const bd_kv_cache &c, const bd
 {
     if (b.n_tokens == 0)
         return 0;
-    return (size_t)make_plan(n_heads, c, b).rows * (c.head_dim * 4 + 8);
+    return cut_bytes(b) + (size_t)make_plan(n_heads, c, b).rows * (c.head_dim * 4 + 8);
 }
 
 hipError_t launch_attention(const uint16_t *q, int64_t q_stride, int32_t n_heads, float scale, const bd_kv_cache &c,
@@ -993,7 +1021,8 @@ hipError_t launch_attention(const uint16_t *q, int64_t q_stride, int32_t n_heads
     a.q = q, a.q_stride = q_stride, a.out = out, a.scale = scale;
     a.k = static_cast<const uint8_t *>(c.k), a.v = static_cast<const uint8_t *>(c.v);
     a.k_scale = c.k_scale, a.v_scale = c.v_scale;
-    a.part_o = static_cast<float *>(workspace);
+    a.cut = static_cast<int64_t *>(workspace);
+    a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + cut_bytes(b));
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + pl.rows * c.head_dim);
     const bool e4m3 = c.dtype == BD_KV_E4M3;
     if (c.head_dim == 64) {

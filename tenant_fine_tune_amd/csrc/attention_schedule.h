@@ -8,10 +8,11 @@
 // a group is either taken with each sequence's own keys, or, where the group
 // is `shared`, once for the rows of all its sequences by the tiled kernel.
 //
-//   streaming kernel: units of kStreamKeys keys of (sequence, key head, row
-//     tile), laid end to end; workgroup w takes units [w * c, (w + 1) * c).
-//     A run of units that a workgroup boundary cuts leaves partial states in
-//     the slots 2w (began before w) and 2w + 1 (goes on after w).
+//   streaming kernel: runs of (sequence, key head, row tile), each kRunCost
+//     units for its beginning and one unit per kStreamKeys keys, laid end to
+//     end; workgroup w takes units [w * c, (w + 1) * c).  A run whose keys a
+//     workgroup boundary cuts leaves partial states in the slots 2w (keys
+//     began before w) and 2w + 1 (they go on after w).
 //   tiled kernel: items (segment, row tile, split, key head); a segment is a
 //     sequence or a shared prefix.  A split segment, and every segment of a
 //     shared group, leaves partial states in planes [split][token][head]:
@@ -25,8 +26,10 @@ namespace bd {
 constexpr int kStreamKeys = 32;      // keys of a streaming unit
 constexpr int kTileKeys = 64;        // keys of a tiled step
 constexpr int kTileRows = 128;       // rows of a tiled item
+constexpr int kRunCost = 4;          // units that a run's beginning and end cost
 constexpr int kMinUnits = 4;         // units that are worth a workgroup: one a wave
 constexpr int kMinTiles = 4;         // key tiles that are worth a split
+constexpr int kItemCost = 5;         // key tiles that a tiled item's beginning and end cost
 constexpr int kSharedNew = 16;       // new tokens a sequence up to which a group is shared
 constexpr int kTiledSlots = 512;     // workgroups of the tiled kernel that run at once
 
@@ -100,9 +103,10 @@ BD_HD int own_seen(const Segment &g, int i)
 
 // ------------------------------------------------------------ streaming kernel
 BD_HD int64_t stream_row_tiles(const Sched &s, const Segment &g) { return cdiv(rows_of(s, g), s.stream_rows); }
+BD_HD int stream_run(const Segment &g) { return kRunCost + key_tiles(g, kStreamKeys); }
 BD_HD int64_t stream_units(const Sched &s, const Segment &g)
 {
-    return g.ntok && streamed(s, g) ? s.p.n_kv * stream_row_tiles(s, g) * key_tiles(g, kStreamKeys) : 0;
+    return g.ntok && streamed(s, g) && g.pre + g.own > 0 ? s.p.n_kv * stream_row_tiles(s, g) * stream_run(g) : 0;
 }
 // Units of a workgroup, of `total` in all.
 BD_HD int64_t stream_chunk(const Sched &s, int64_t total)
@@ -128,15 +132,21 @@ BD_HD int64_t tiled_work(const Sched &s, const Segment &g)
 {
     return s.p.n_kv * tiled_row_tiles(s, g) * key_tiles(g, kTileKeys);
 }
-// Key tiles of a split, where all segments together have `work`.
-BD_HD int64_t tiled_depth(const Sched &, int64_t work)
+// Time of the whole work, in key tiles, if each of `items` unsplit items with
+// `work` key tiles in all were cut into k.
+BD_HD float tiled_time(int64_t items, int64_t work, int k)
 {
-    const int64_t d = cdiv(work, kTiledSlots);
+    return ceilf((float)items * k / kTiledSlots) * (ceilf((float)work / ((float)items * k)) + kItemCost);
+}
+// Key tiles of a split where items are cut into k on the average.
+BD_HD int64_t tiled_depth(int64_t items, int64_t work, int k)
+{
+    const int64_t d = items > 0 ? cdiv(work, items * k) : 0;
     return d < kMinTiles ? kMinTiles : d;
 }
 BD_HD int tiled_splits(const Sched &s, const Segment &g, int64_t depth)
 {
-    const int64_t n = cdiv(key_tiles(g, kTileKeys), depth);
+    const int64_t n = (key_tiles(g, kTileKeys) + depth / 2) / depth;
     return (int)(n < 1 ? 1 : n > s.splits ? s.splits : n);
 }
 BD_HD int64_t tiled_items(const Sched &s, const Segment &g, int64_t depth)

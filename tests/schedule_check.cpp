@@ -141,8 +141,13 @@ int main()
                 EXPECT(seq < p.b.n_seqs);
                 const Segment g = sequence(s, gr, seq);
                 const int tiles = key_tiles(g, kStreamKeys);
-                const int64_t run = (at - begin[seq]) / tiles, rt = stream_row_tiles(s, g);
-                const int t0 = (int)((at - begin[seq]) % tiles), t1 = (int)std::min<int64_t>(tiles, t0 + end - at);
+                const int len = stream_run(g);
+                const int64_t run = (at - begin[seq]) / len, rt = stream_row_tiles(s, g);
+                const int from = (int)((at - begin[seq]) % len), to = (int)std::min<int64_t>(len, from + end - at);
+                const int t0 = std::max(from - kRunCost, 0), t1 = to - kRunCost;
+                at += to - from;
+                if (t0 >= t1)
+                    continue;
                 const int head = (int)(run / rt);
                 EXPECT(head < p.n_kv);
                 const int64_t row0 = run % rt * s.stream_rows;
@@ -159,18 +164,24 @@ int main()
                         ++part[pr];
                     }
                 }
-                at += t1 - t0;
             }
         }
         EXPECT(total <= chunk * s.stream_wgs);
         // tiled kernel
-        int64_t work = 0, depth;
+        int64_t work = 0, items_all = 0, depth = INT_MAX;
         const int n_seg = p.b.n_seqs + p.b.n_groups;
         for (int i = 0; i < n_seg; ++i) {
             const Segment g = tiled_segment(s, gr, i);
             work += g.ntok ? tiled_work(s, g) : 0;
+            items_all += g.ntok ? p.n_kv * tiled_row_tiles(s, g) : 0;
         }
-        depth = tiled_depth(s, work);
+        if (s.splits > 1) {
+            int best = 1;
+            for (int k = 2; k <= s.splits; ++k)
+                if (tiled_time(items_all, work, k) < tiled_time(items_all, work, best))
+                    best = k;
+            depth = tiled_depth(items_all, work, best);
+        }
         EXPECT(s.tiled || work == 0);
         for (int seg = 0; seg < n_seg; ++seg) {
             const Segment g = tiled_segment(s, gr, seg);
@@ -216,7 +227,7 @@ int main()
                         const int tiles = key_tiles(g, kStreamKeys), head = h / s.group;
                         const int64_t row = (tok - g.tok0) * s.group + h % s.group;
                         if (tiles) {
-                            const int64_t u0 = begin[seq] + (head * stream_row_tiles(s, g) + row / s.stream_rows) * tiles;
+                            const int64_t u0 = begin[seq] + kRunCost + (head * stream_row_tiles(s, g) + row / s.stream_rows) * stream_run(g);
                             const int64_t w0 = u0 / chunk, n = (u0 + tiles - 1) / chunk - w0 + 1;
                             if (n == 1 && !g.shared)
                                 done = true;
