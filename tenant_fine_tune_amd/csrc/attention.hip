@@ -30,7 +30,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kSchedMfma = 0x008, kSchedLdsRead = 0x100;   // masks of sched_group_barrier
 
 struct AttnArgs {
     Sched s;
@@ -714,27 +713,34 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
             bool masked = false;
             uint64_t held = 0;
             if (active) {
-                held = __ballot(key_held[buf][lane] != 0);
+                // kAhead fragments are read ahead of the matrix instructions; the
+                // scheduling fences keep the compiler from drawing a read to its use
+                constexpr int kAhead = 6;
                 const uint16_t *kl = kt[buf] + col * KR + half * 8;
+                bf16x8 kf[kAhead];
+                const auto read_k = [&](int i) {
+                    kf[i % kAhead] = as_bf16x8(*reinterpret_cast<const uint4 *>(kl + (i & 1) * 32 * KR + (i >> 1) * 16));
+                };
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    read_k(i);
+                const uint8_t key_here = key_held[buf][lane];
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         x[b][r] = 0.0f;
+                __builtin_amdgcn_s_setprio(1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            as_bf16x8(*reinterpret_cast<const uint4 *>(kl + b * 32 * KR + k * 16)), q[k], x[b], 0, 0, 0);
-                // four fragments ahead of the matrix instructions
-                __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 5, 0);
-#pragma unroll
-                for (int k = 0; k < 2 * KS - 4; ++k) {
-                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+                for (int i = 0; i < 2 * KS; ++i) {
+                    x[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % kAhead], q[i >> 1], x[i & 1], 0, 0, 0);
+                    if (i + kAhead < 2 * KS)
+                        read_k(i + kAhead);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 4, 0);
+                __builtin_amdgcn_s_setprio(0);
+                held = __ballot(key_here != 0);
                 masked = held != ~0ull || (own && j0 + kTileKeys > least);
             }
             if (t + 1 < t1) {
@@ -744,10 +750,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
             if (active) {
                 // keys 16 i + 4 half + 0..3 and + 8 of column 32 d + col
                 const uint16_t *vl = vt[buf] + (half * 4 + ((lane & 15) >> 2)) * VR + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-                const auto read_v = [&](int i, int d) {
-                    const u32x2 lo = read_tr(vl + i * 16 * VR + d * 32), hi = read_tr(vl + (i * 16 + 8) * VR + d * 32);
-                    return as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1]));
+                bf16x8 vf[2][DB];
+                const auto read_v = [&](int i) {
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const uint16_t *from = vl + i * 16 * VR + d * 32;
+                        const u32x2 lo = read_tr(from), hi = read_tr(from + 8 * VR);
+                        vf[i & 1][d] = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1]));
+                    }
                 };
+                read_v(0);
+                __builtin_amdgcn_sched_barrier(0);
                 if (masked) {
                     const uint64_t ok = (held & first_bits64(left)) >> half * 4;
                     const uint32_t word[2] = {(uint32_t)ok, (uint32_t)(ok >> 32)};
@@ -775,21 +788,33 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
                         o[d] *= keep;
                 }
                 const float mu = m == -INFINITY ? 0.0f : m;
+                // the weights of the next 16 keys are formed between the matrix
+                // instructions of these
+                float e[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    e[r] = exp2_(fmaf(x[0][r], sc, -mu));
+                bf16x8 pf = weights(e, l);
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    bf16x8 vf[DB];
+                    if (i < 3)
+                        read_v(i + 1);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        vf[d] = read_v(i, d);
-                    float e[8];
+                    for (int d = 0; d < DB; ++d) {
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i & 1][d], pf, o[d], 0, 0, 0);
+                        if (i < 3) {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        e[r] = exp2_(fmaf(x[i >> 1][(i & 1) * 8 + r], sc, -mu));
-                    const bf16x8 pf = weights(e, l);
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[d], pf, o[d], 0, 0, 0);
+                            for (int r = d * (8 / DB); r < (d + 1) * (8 / DB); ++r)
+                                e[r] = exp2_(fmaf(x[(i + 1) >> 1][((i + 1) & 1) * 8 + r], sc, -mu));
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                    if (i < 3)
+                        pf = weights(e, l);
                 }
+                __builtin_amdgcn_s_setprio(0);
                 if (partial(t) && (any_bad[buf][0] | any_bad[buf][1] | any_bad[buf][2] | any_bad[buf][3])) {
 #pragma unroll 1
                     for (int key = 0; key < kTileKeys; ++key)
@@ -844,22 +869,27 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
 
 // ------------------------------------------------------------------------ join
 //
-// Joins the partial states of a token's heads, one wave a head; writes the
-// zero rows of tokens that see nothing; leaves finished rows alone.
-template <int D>
+// Joins the partial states of a token's heads and writes the zero rows of
+// tokens that see nothing; finished rows are left alone.  Latency bound: 16
+// lanes take a head, so a wave has four heads' states on the way, and where
+// BY_PARTS (few tokens, perhaps many states a head) the four waves share the
+// states of the same four heads.
+template <int D, bool BY_PARTS>
 __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
 {
-    constexpr int N = D / 64;
+    constexpr int N = D / 64;      // 16-byte pieces of a lane, 64 columns apart
     __shared__ Groups groups;
+    __shared__ float2 wave_ml[kWaves][4];
+    __shared__ f32x4 wave_o[kWaves][4][D / 4];
     const Sched &s = a.s;
     const Paged &p = s.p;
     const int64_t tok = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15, grp = lane >> 4;
     const int64_t slots = 2 * (int64_t)s.stream_wgs * s.stream_rows, plane = p.b.n_tokens * s.n_heads;
 
     const int seq = seq_of(p, tok);
     // parts of own keys: planes [0, own_parts), or the slots of workgroups first_wg .. where `slotted`
-    int own_parts = 0, prefix_parts = 0;
+    int own_parts = 0, prefix_parts = 0, tiles = 0;
     bool by_stream = false;
     Segment g;
     int64_t units0 = 0, chunk = 1;
@@ -870,6 +900,7 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
         const int64_t depth = s.tiled ? a.cut[0] : 1;
         chunk = a.cut[1];
         units0 = a.cut[2 + seq];
+        tiles = key_tiles(g, kStreamKeys);
         if (!by_stream) {
             own_parts = tiled_splits(s, g, depth);
             if (own_parts == 1 && !g.shared)
@@ -878,31 +909,36 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
         if (g.shared)
             prefix_parts = tiled_splits(s, prefix(s, groups, g.group), depth);
     }
-    const int tiles = seq >= 0 ? key_tiles(g, kStreamKeys) : 0;
-    for (int h = blockIdx.y * kWaves + wave; h < s.n_heads; h += gridDim.y * kWaves) {
+    constexpr int kHeads = BY_PARTS ? 4 : 4 * kWaves;      // heads of a workgroup at a time
+    for (int h0 = blockIdx.y * kHeads; h0 < s.n_heads; h0 += gridDim.y * kHeads) {
+        const int h = h0 + (BY_PARTS ? 0 : wave * 4) + grp;
+        bool mine = h < s.n_heads;
         const int64_t cell_out = tok * s.n_heads + h;
-        int64_t first_wg = 0, row_in = 0;
-        int parts = own_parts;
+        int64_t first_wg = 0;
+        int parts = own_parts, row_in = 0;
         bool slotted = false;
-        if (by_stream && tiles) {
-            const int head = h / s.group;
-            const int64_t row = (tok - g.tok0) * s.group + h - head * s.group;
+        if (by_stream && tiles && mine) {
+            const int head = h / s.group, row = (int)(tok - g.tok0) * s.group + h - head * s.group;
             const int64_t u0 = units0 + kRunCost +
-                               (head * stream_row_tiles(s, g) + (int)row / s.stream_rows) * stream_run(g);
+                               (head * stream_row_tiles(s, g) + row / s.stream_rows) * stream_run(g);
             first_wg = quotient(u0, chunk);
             parts = (int)(quotient(u0 + tiles - 1, chunk) - first_wg) + 1;
             slotted = parts > 1;
-            row_in = (int)row % s.stream_rows;
-            if (!slotted && !g.shared)
-                continue;
+            row_in = row % s.stream_rows;
+            mine = slotted || g.shared;
         }
-        float m = -INFINITY, l = 0.0f, o[N];
+        const int total = mine ? parts + prefix_parts : 0;
+        int most = total;
+        most = max(most, __shfl_xor(most, 16));
+        most = max(most, __shfl_xor(most, 32));
+        float m = -INFINITY, l = 0.0f;
+        f32x4 o[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            o[i] = 0.0f;
-        const int total = parts + prefix_parts;
-        for (int b = 0; b < total; b += 64) {
-            const int i = b + lane;
+            o[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        // lane `sub` holds a part's m and l, then the 16 lanes add the parts' values
+        for (int b = BY_PARTS ? wave * 16 : 0; b < most; b += BY_PARTS ? 16 * kWaves : 16) {
+            const int i = b + sub;
             int64_t pr = 0;
             float2 ml = make_float2(-INFINITY, 0.0f);
             if (i < total) {
@@ -916,7 +952,7 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
             }
             float mx = ml.x;
 #pragma unroll
-            for (int w = 32; w > 0; w >>= 1)
+            for (int w = 8; w > 0; w >>= 1)
                 mx = fmaxf(mx, __shfl_xor(mx, w));
             const float mn = fmaxf(m, mx);
             // a part without keys has m = -inf and l = 0 (NaN where its scores were)
@@ -924,31 +960,67 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
             const float e = none ? 0.0f : exp2_(ml.x - mn), keep = m == -INFINITY ? 0.0f : exp2_(m - mn);
             float sum = none ? 0.0f : e * ml.y;
 #pragma unroll
-            for (int w = 32; w > 0; w >>= 1)
+            for (int w = 8; w > 0; w >>= 1)
                 sum += __shfl_xor(sum, w);
             l = l * keep + sum;
             m = mn;
 #pragma unroll
-            for (int i2 = 0; i2 < N; ++i2)
-                o[i2] *= keep;
-            // eight states' loads in flight; lanes past the last part hold `none` and row 0
-            for (int j = 0; j < min(64, total - b); j += 8)
+            for (int c = 0; c < N; ++c)
+                o[c] *= keep;
+            for (int j0 = 0; j0 < min(16, most - b); j0 += 4)
 #pragma unroll
-                for (int j8 = 0; j8 < 8; ++j8) {
-                    const float ej = __shfl(e, j + j8);
-                    const int64_t row = __shfl(pr, j + j8);
-                    const bool skip = __shfl((int)none, j + j8);
-                    const float *src = a.part_o + row * D + lane * N;
+                for (int j4 = 0; j4 < 4; ++j4) {
+                    const int from = (lane & 48) + j0 + j4;
+                    const float ej = __shfl(e, from);
+                    const int64_t row = __shfl(pr, from);     // row 0 where there is no such part
+                    const bool skip = __shfl((int)none, from);
 #pragma unroll
-                    for (int i2 = 0; i2 < N; ++i2)
-                        o[i2] += skip ? 0.0f : ej * src[i2];
+                    for (int c = 0; c < N; ++c) {
+                        const f32x4 v = *reinterpret_cast<const f32x4 *>(a.part_o + row * D + c * 64 + sub * 4);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            o[c][r] += skip ? 0.0f : ej * v[r];
+                    }
                 }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        if (N == 2)
-            *reinterpret_cast<uint32_t *>(a.out + cell_out * D + lane * 2) = pack_bf16x2(o[0] * inv, o[N - 1] * inv);
-        else
-            a.out[cell_out * D + lane] = to_bf16(o[0] * inv);
+        if (BY_PARTS) {
+            if (sub == 0)
+                wave_ml[wave][grp] = make_float2(m, l);
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+                wave_o[wave][grp][c * 16 + sub] = o[c];
+            __syncthreads();
+            float mm = -INFINITY;
+            l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                mm = fmaxf(mm, wave_ml[w][grp].x);
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+                o[c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float2 ml = wave_ml[w][grp];
+                if (ml.x == -INFINITY && !(ml.y != ml.y))
+                    continue;
+                const float e = exp2_(ml.x - mm);
+                l += e * ml.y;
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+                    o[c] += wave_o[w][grp][c * 16 + sub] * e;
+            }
+            __syncthreads();
+        }
+        if (mine && (!BY_PARTS || wave == 0)) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                u32x2 w;
+                w[0] = pack_bf16x2(o[c][0] * inv, o[c][1] * inv);
+                w[1] = pack_bf16x2(o[c][2] * inv, o[c][3] * inv);
+                *reinterpret_cast<u32x2 *>(a.out + cell_out * D + c * 64 + sub * 4) = w;
+            }
+        }
     }
 }
 
@@ -998,9 +1070,12 @@ void start(const AttnArgs &a, const Plan &pl, hipStream_t st)
         attention_stream<D, E4M3, 1><<<dim3(s.stream_wgs), kThreads, 0, st>>>(a);
     else
         attention_stream<D, E4M3, 2><<<dim3(s.stream_wgs), kThreads, 0, st>>>(a);
-    const int64_t T = s.p.b.n_tokens, waves = (s.n_heads + kWaves - 1) / kWaves;
-    const int64_t y = 8192 / T;
-    attention_join<D><<<dim3((unsigned)T, (unsigned)(y < 1 ? 1 : y > waves ? waves : y)), kThreads, 0, st>>>(a);
+    // a workgroup for every four heads where tokens are few, else for sixteen
+    const unsigned T = (unsigned)s.p.b.n_tokens, heads = (unsigned)s.n_heads;
+    if (T <= 64)
+        attention_join<D, true><<<dim3(T, (heads + 3) / 4), kThreads, 0, st>>>(a);
+    else
+        attention_join<D, false><<<dim3(T, T <= 2048 ? (heads + 15) / 16 : 1), kThreads, 0, st>>>(a);
 }
 
 }  // namespace
