@@ -224,8 +224,19 @@ struct Listing {
 // piece of LDS; no barrier until the workgroup's run of one key head ends and
 // the four waves' states are joined.  Eight waves a CU with 16 KB each on the
 // way cover the memory latency.
+template <int D, int NB>
+struct StreamLds {
+    static constexpr int kJoin = kWaves * 16 * NB * (D + 4) * 4, kStage = kWaves * kStreamKeys * Stride<D>::v_stream * 2;
+    __attribute__((aligned(16))) uint8_t tiles[kJoin > kStage ? kJoin : kStage];
+    uint8_t bad[kWaves][kStreamKeys][D / 8];
+    float2 wave_ml[kWaves][16 * NB];
+    Scan scan;
+    Located found;
+    Groups groups;
+};
+
 template <int D, bool E4M3, int NB>
-__global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
+__device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> &sh, int block)
 {
     constexpr int R = 16 * NB, KS = D / 32, DB = D / 16;
     constexpr int ES = E4M3 ? 1 : 2;                 // bytes of a cached number
@@ -234,24 +245,20 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
     constexpr int NV = kStreamKeys * LPR / 64, RPI = 64 / LPR;
     constexpr int VS = Stride<D>::v_stream;
     constexpr int OROW = D + 4;                      // padded row of the join
-    constexpr int kJoin = kWaves * R * OROW * 4, kStage = kWaves * kStreamKeys * VS * 2;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kJoin > kStage ? kJoin : kStage];
-    __shared__ uint8_t bad[kWaves][kStreamKeys][D / 8];
-    __shared__ float2 wave_ml[kWaves][R];
-    __shared__ Scan scan;
-    __shared__ Located found;
-    __shared__ Groups groups;
+    auto &bad = sh.bad;
+    auto &wave_ml = sh.wave_ml;
+    auto &groups = sh.groups;
 
     const Sched &s = a.s;
     const Paged &p = s.p;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
     fill_groups(s, groups);
     const auto size = [&](int i) { return stream_units(s, sequence(s, groups, i)); };
-    const Listing list(p.b.n_seqs, size, scan);
+    const Listing list(p.b.n_seqs, size, sh.scan);
     const int64_t chunk = stream_chunk(s, list.total);
-    int64_t at = blockIdx.x * chunk;
+    int64_t at = block * chunk;
     const int64_t end = min(list.total, at + chunk);
-    if (blockIdx.x == 0) {
+    if (block == 0) {
         if (threadIdx.x == 0)
             a.cut[1] = chunk;
         int64_t b = list.before;
@@ -262,12 +269,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
     }
     if (at >= end)
         return;
-    const Located loc = list.locate(at, &found);
+    const Located loc = list.locate(at, &sh.found);
     int seq = loc.first;
     int64_t base = loc.base;
     Segment g = sequence(s, groups, seq);
-    uint16_t *vt = reinterpret_cast<uint16_t *>(lds) + wave * kStreamKeys * VS;
-    float *oj = reinterpret_cast<float *>(lds);
+    uint16_t *vt = reinterpret_cast<uint16_t *>(sh.tiles) + wave * kStreamKeys * VS;
+    float *oj = reinterpret_cast<float *>(sh.tiles);
 
     while (at < end) {
         for (int64_t units; base + (units = stream_units(s, g)) <= at;) {
@@ -468,7 +475,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
         }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == tiles;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0 ? 1 : 0);
+        const int64_t slot = 2 * (int64_t)block + (t0 == 0 ? 1 : 0);
         const float vs = E4M3 && a.v_scale ? a.v_scale[head] : 1.0f;
         for (int u = threadIdx.x; u < R * (D / 4); u += kThreads) {
             const int r = u / (D / 4), c = u % (D / 4) * 4, row = row0 + r;
@@ -514,20 +521,30 @@ __global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
 // a wave, and walks 64-key tiles of K and V that all four waves read from LDS;
 // a tile's loads are in registers one step ahead, and LDS holds two tiles, so
 // a step has one barrier.
+template <int D>
+struct TiledLds {
+    __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * Stride<D>::k], vt[2][kTileKeys * Stride<D>::v];
+    uint8_t key_held[2][kTileKeys], bad[2][kTileKeys][D / 8];
+    uint32_t any_bad[2][kWaves];
+    Scan scan, scan2;
+    Located found;
+    Groups groups;
+};
+
 template <int D, bool E4M3>
-__global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
+__device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, int block, int blocks)
 {
     constexpr int KS = D / 16, DB = D / 32;
     constexpr int ES = E4M3 ? 1 : 2;
     constexpr int NL = D * ES / 64;   // loads of a thread, K and V each: four threads a key, 64 bytes a load
     static_assert(kThreads == 4 * kTileKeys, "four threads a key");
     constexpr int KR = Stride<D>::k, VR = Stride<D>::v;
-    __shared__ __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * KR], vt[2][kTileKeys * VR];
-    __shared__ uint8_t key_held[2][kTileKeys], bad[2][kTileKeys][D / 8];
-    __shared__ uint32_t any_bad[2][kWaves];
-    __shared__ Scan scan, scan2;
-    __shared__ Located found;
-    __shared__ Groups groups;
+    auto &kt = sh.kt;
+    auto &vt = sh.vt;
+    auto &key_held = sh.key_held;
+    auto &bad = sh.bad;
+    auto &any_bad = sh.any_bad;
+    auto &groups = sh.groups;
 
     const Sched &s = a.s;
     const Paged &p = s.p;
@@ -544,7 +561,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
                 items += p.n_kv * tiled_row_tiles(s, g);
             }
         }
-        sum_block(work, items, scan, scan2);
+        sum_block(work, items, sh.scan, sh.scan2);
         // lane k - 1 tries k
         float best = lane < s.splits && items > 0 ? tiled_time(items, work, lane + 1) : INFINITY;
         const float mine = best;
@@ -553,13 +570,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
             best = fminf(best, __shfl_xor(best, o));
         depth = tiled_depth(items, work, __ffsll(__ballot(mine == best)));
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0)
+    if (block == 0 && threadIdx.x == 0)
         a.cut[0] = depth;
     const auto size = [&](int i) { return tiled_items(s, tiled_segment(s, groups, i), depth); };
-    const Listing<decltype(size)> list(n_seg, size, scan);
+    const Listing<decltype(size)> list(n_seg, size, sh.scan);
 
-    for (int64_t item = blockIdx.x; item < list.total; item += gridDim.x) {
-        const Located loc = list.locate(item, &found);
+    for (int64_t item = block; item < list.total; item += blocks) {
+        const Located loc = list.locate(item, &sh.found);
         int seg = loc.first;
         int64_t base = loc.base;
         Segment g;
@@ -867,6 +884,32 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
     }
 }
 
+// ---------------------------------------------------------------------- kernels
+
+template <int D, bool E4M3, int NB>
+__global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
+{
+    __shared__ StreamLds<D, NB> sh;
+    stream_body<D, E4M3, NB>(a, sh, blockIdx.x);
+}
+
+// Both at once where a call may have work for both: the streaming workgroups
+// come first, one for each CU, and the tiled ones fill the other half, so that
+// the one's loads run under the other's matrix instructions.
+template <int D, bool E4M3, int NB>
+__global__ __launch_bounds__(kThreads, 2) void attention_mixed(AttnArgs a)
+{
+    __shared__ union {
+        StreamLds<D, NB> stream;
+        TiledLds<D> tiled;
+    } sh;
+    const int block = blockIdx.x, streaming = a.s.stream_wgs;
+    if (block < streaming)
+        stream_body<D, E4M3, NB>(a, sh.stream, block);
+    else
+        tiled_body<D, E4M3>(a, sh.tiled, block - streaming, gridDim.x - streaming);
+}
+
 // ------------------------------------------------------------------------ join
 //
 // Joins the partial states of a token's heads and writes the zero rows of
@@ -875,7 +918,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_tiled(AttnArgs a)
 // BY_PARTS (few tokens, perhaps many states a head) the four waves share the
 // states of the same four heads.
 template <int D, bool BY_PARTS>
-__global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
+__global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a, int tokens)
 {
     constexpr int N = D / 64;      // 16-byte pieces of a lane, 64 columns apart
     __shared__ Groups groups;
@@ -883,28 +926,33 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
     __shared__ f32x4 wave_o[kWaves][4][D / 4];
     const Sched &s = a.s;
     const Paged &p = s.p;
-    const int64_t tok = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15, grp = lane >> 4;
     const int64_t slots = 2 * (int64_t)s.stream_wgs * s.stream_rows, plane = p.b.n_tokens * s.n_heads;
 
-    const int seq = seq_of(p, tok);
+    const int64_t tok0 = (int64_t)blockIdx.x * tokens;
+    const int64_t depth = s.tiled ? a.cut[0] : 1, chunk = a.cut[1];
+    fill_groups(s, groups);
+    int seq = seq_of(p, tok0);
+    for (int64_t tok = tok0; tok < min(tok0 + tokens, p.b.n_tokens); ++tok) {
+    if (seq < 0 || tok >= seq_begin(p, seq + 1))
+        seq = tok == tok0 ? seq : seq_of(p, tok);
     // parts of own keys: planes [0, own_parts), or the slots of workgroups first_wg .. where `slotted`
     int own_parts = 0, prefix_parts = 0, tiles = 0;
     bool by_stream = false;
     Segment g;
-    int64_t units0 = 0, chunk = 1;
+    int64_t units0 = 0;
     if (seq >= 0) {
-        fill_groups(s, groups);
         g = sequence(s, groups, seq);
         by_stream = streamed(s, g);
-        const int64_t depth = s.tiled ? a.cut[0] : 1;
-        chunk = a.cut[1];
         units0 = a.cut[2 + seq];
         tiles = key_tiles(g, kStreamKeys);
         if (!by_stream) {
             own_parts = tiled_splits(s, g, depth);
-            if (own_parts == 1 && !g.shared)
-                return;
+            if (own_parts == 1 && !g.shared) {
+                // finished, and so are the sequence's other tokens
+                tok = (int64_t)g.tok0 + g.ntok - 1;
+                continue;
+            }
         }
         if (g.shared)
             prefix_parts = tiled_splits(s, prefix(s, groups, g.group), depth);
@@ -1022,13 +1070,14 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a)
             }
         }
     }
+    }
 }
 
 // ------------------------------------------------------------------------ host
 
 struct Plan {
     Sched s;
-    int64_t tiled_grid, rows;     // rows of partial states
+    int64_t grid, rows;     // workgroups, rows of partial states
 };
 
 size_t cut_bytes(const bd_batch &b) { return (size_t)(2 + b.n_seqs + 1) / 2 * 16; }
@@ -1042,10 +1091,10 @@ Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
     const int64_t T = b.n_tokens;
     // 32 rows a streaming tile; 16 where the hint says that no sequence has more
     const int64_t most = b.max_new > 0 ? (int64_t)b.max_new * s.group : T > b.n_seqs ? INT_MAX : s.group;
-    s.stream_rows = most <= 16 ? 16 : 32;
     s.tiled = b.n_groups > 0 || most > 32;
+    s.stream_rows = most <= 16 ? 16 : 32;
     s.few = s.tiled ? 32 : INT_MAX;
-    s.stream_wgs = 512;
+    s.stream_wgs = s.tiled ? 256 : 512;
     // enough splits that row tiles x key heads x splits fill the chip twice
     const int64_t tiles = cdiv(T * s.group, kTileRows) * c.n_kv_heads;
     const int64_t want = cdiv(2 * kTiledSlots, tiles);
@@ -1056,7 +1105,8 @@ Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
     const int64_t full = T * s.group / kTileRows;
     const int64_t row_tiles = full + (b.n_seqs < T ? b.n_seqs : T) + (b.n_groups > 0 ? full + b.n_groups : 0);
     const int64_t items = row_tiles * c.n_kv_heads * s.splits, cap = s.splits > 1 ? 2 * kTiledSlots : INT_MAX;
-    pl.tiled_grid = items < 1 ? 1 : items < cap ? items : cap;
+    const int64_t tiled_wgs = items < s.stream_wgs ? s.stream_wgs : items < cap ? items : cap;
+    pl.grid = s.stream_wgs + (s.tiled ? tiled_wgs : 0);
     return pl;
 }
 
@@ -1064,18 +1114,23 @@ template <int D, bool E4M3>
 void start(const AttnArgs &a, const Plan &pl, hipStream_t st)
 {
     const Sched &s = a.s;
-    if (s.tiled)
-        attention_tiled<D, E4M3><<<dim3((unsigned)pl.tiled_grid), kThreads, 0, st>>>(a);
-    if (s.stream_rows == 16)
-        attention_stream<D, E4M3, 1><<<dim3(s.stream_wgs), kThreads, 0, st>>>(a);
+    const dim3 grid((unsigned)pl.grid);
+    if (s.tiled && s.stream_rows == 16)
+        attention_mixed<D, E4M3, 1><<<grid, kThreads, 0, st>>>(a);
+    else if (s.tiled)
+        attention_mixed<D, E4M3, 2><<<grid, kThreads, 0, st>>>(a);
+    else if (s.stream_rows == 16)
+        attention_stream<D, E4M3, 1><<<grid, kThreads, 0, st>>>(a);
     else
-        attention_stream<D, E4M3, 2><<<dim3(s.stream_wgs), kThreads, 0, st>>>(a);
+        attention_stream<D, E4M3, 2><<<grid, kThreads, 0, st>>>(a);
     // a workgroup for every four heads where tokens are few, else for sixteen
     const unsigned T = (unsigned)s.p.b.n_tokens, heads = (unsigned)s.n_heads;
     if (T <= 64)
-        attention_join<D, true><<<dim3(T, (heads + 3) / 4), kThreads, 0, st>>>(a);
+        attention_join<D, true><<<dim3(T, (heads + 3) / 4), kThreads, 0, st>>>(a, 1);
+    else if (T <= 2048)
+        attention_join<D, false><<<dim3(T, (heads + 15) / 16), kThreads, 0, st>>>(a, 1);
     else
-        attention_join<D, false><<<dim3(T, T <= 2048 ? (heads + 15) / 16 : 1), kThreads, 0, st>>>(a);
+        attention_join<D, false><<<dim3((T + 15) / 16), kThreads, 0, st>>>(a, 16);
 }
 
 }  // namespace
