@@ -104,6 +104,18 @@ __device__ __forceinline__ void lds_order()
     asm volatile("" ::: "memory");
 }
 
+// The wave's number in the workgroup, as a value the compiler knows to be the
+// same in all of its lanes.
+__device__ __forceinline__ int wave_of_thread() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+
+// The larger of lane l's and lane l ^ 32's value.
+__device__ __forceinline__ float max_of_halves(float x)
+{
+    const uint32_t b = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Where a column of V holds a number that is not finite, a weight of zero does
@@ -251,7 +263,7 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
 
     const Sched &s = a.s;
     const Paged &p = s.p;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_of_thread(), col = lane & 15, quad = lane >> 4;
     fill_groups(s, groups);
     const auto size = [&](int i) { return stream_units(s, sequence(s, groups, i)); };
     const Listing list(p.b.n_seqs, size, sh.scan);
@@ -525,7 +537,7 @@ template <int D>
 struct TiledLds {
     __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * Stride<D>::k], vt[2][kTileKeys * Stride<D>::v];
     uint8_t key_held[2][kTileKeys], bad[2][kTileKeys][D / 8];
-    uint32_t any_bad[2][kWaves];
+    int hole[2][kWaves], any_bad[2][kWaves];
     Scan scan, scan2;
     Located found;
     Groups groups;
@@ -544,11 +556,12 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
     auto &key_held = sh.key_held;
     auto &bad = sh.bad;
     auto &any_bad = sh.any_bad;
+    auto &hole = sh.hole;
     auto &groups = sh.groups;
 
     const Sched &s = a.s;
     const Paged &p = s.p;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
+    const int lane = threadIdx.x & 63, wave = wave_of_thread(), col = lane & 31, half = lane >> 5;
     const int n_seg = p.b.n_seqs + p.b.n_groups;
     int64_t depth = INT_MAX;
     fill_groups(s, groups);
@@ -574,6 +587,13 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         a.cut[0] = depth;
     const auto size = [&](int i) { return tiled_items(s, tiled_segment(s, groups, i), depth); };
     const Listing<decltype(size)> list(n_seg, size, sh.scan);
+
+    // Tiles are numbered over all items of the workgroup.  A wave that stages
+    // keys without a cell, or values that are not finite, leaves the tile's
+    // number in its flag; nothing is written for the other tiles.
+    if (threadIdx.x < 2 * kWaves)
+        (&hole[0][0])[threadIdx.x] = (&any_bad[0][0])[threadIdx.x] = -1;
+    int number = 0;
 
     for (int64_t item = block; item < list.total; item += blocks) {
         const Located loc = list.locate(item, &sh.found);
@@ -663,6 +683,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         const auto partial = [&](int t) { return t >= pre_tiles && (t - pre_tiles + 1) * kTileKeys > least_all; };
         const int ldc = part * (E4M3 ? 2 : 1);                     // first of a load's 8-column pieces
         constexpr int PIECES = E4M3 ? 2 : 1, STEP = 4 * PIECES;
+        const int num0 = number - t0;                              // tile t has number num0 + t
         const auto stage_k = [&](int t) {
             uint4 *dst = reinterpret_cast<uint4 *>(kt[t & 1] + ldr * KR + ldc * 8);
 #pragma unroll
@@ -673,13 +694,25 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                 } else {
                     dst[i * STEP] = in[i];
                 }
-            if (part == 0)
+            if (__any(cell < 0)) {
                 key_held[t & 1][ldr] = cell >= 0;
+                hole[t & 1][wave] = num0 + t;
+            }
         };
         const auto stage_v = [&](int t) {
             const int buf = t & 1;
             uint4 *dst = reinterpret_cast<uint4 *>(vt[buf] + ldr * VR + ldc * 8);
-            const bool check = partial(t), hole = __any(cell < 0);
+            if (!partial(t) && !__any(cell < 0)) {
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+                    if (E4M3) {
+                        dst[i * STEP] = e4m3x8_to_bf16(in[i].x, in[i].y);
+                        dst[i * STEP + 1] = e4m3x8_to_bf16(in[i].z, in[i].w);
+                    } else {
+                        dst[i * STEP] = in[i];
+                    }
+                return;
+            }
             uint32_t found_bad = 0;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
@@ -688,9 +721,9 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                     v[0] = e4m3x8_to_bf16(in[i].x, in[i].y), v[1] = e4m3x8_to_bf16(in[i].z, in[i].w);
 #pragma unroll
                 for (int e = 0; e < PIECES; ++e) {
-                    if (hole && cell < 0)
+                    if (cell < 0)
                         v[e] = make_uint4(0, 0, 0, 0);
-                    if (check) {
+                    if (partial(t)) {
                         const uint32_t bits = take_nonfinite(v[e]);
                         bad[buf][ldr][ldc + i * STEP + e] = (uint8_t)bits;
                         found_bad |= bits;
@@ -698,11 +731,8 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                     dst[i * STEP + e] = v[e];
                 }
             }
-            if (check) {
-                const bool any = __any(found_bad != 0);
-                if (lane == 0)
-                    any_bad[buf][wave] = any;
-            }
+            if (__any(found_bad != 0))
+                any_bad[buf][wave] = num0 + t;
         };
         // q has to be there before the loop: its wait inside would be one for all loads in flight
         wait_vmcnt<0>();
@@ -741,7 +771,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
                     read_k(i);
-                const uint8_t key_here = key_held[buf][lane];
+                const int4 flags = *reinterpret_cast<const int4 *>(hole[buf]);
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -757,7 +787,12 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 __builtin_amdgcn_s_setprio(0);
-                held = __ballot(key_here != 0);
+                held = ~0ull;
+                const int now = num0 + t;
+                if (flags.x == now || flags.y == now || flags.z == now || flags.w == now)
+                    held = __ballot(key_held[buf][lane] != 0) | (flags.x == now ? 0 : 0xFFFFull) |
+                           (flags.y == now ? 0 : 0xFFFFull << 16) | (flags.z == now ? 0 : 0xFFFFull << 32) |
+                           (flags.w == now ? 0 : 0xFFFFull << 48);
                 masked = held != ~0ull || (own && j0 + kTileKeys > least);
             }
             if (t + 1 < t1) {
@@ -793,7 +828,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         mx = fmaxf(mx, x[b][r]);
-                mx = fmaxf(mx, __shfl_xor(mx, 32)) * sc;
+                mx = max_of_halves(mx) * sc;
                 // the maximum follows only where it grew by more than 2^8: weights
                 // up to 2^8 are as exact, and most tiles need no rescaling
                 if (__any(mx > m + 8.0f)) {
@@ -832,12 +867,16 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                         pf = weights(e, l);
                 }
                 __builtin_amdgcn_s_setprio(0);
-                if (partial(t) && (any_bad[buf][0] | any_bad[buf][1] | any_bad[buf][2] | any_bad[buf][3])) {
+                const int now = num0 + t;
+                bool some = false;
+                for (int w = 0; w < kWaves; ++w)
+                    some |= partial(t) && any_bad[buf][w] == now;
+                if (some) {
 #pragma unroll 1
                     for (int key = 0; key < kTileKeys; ++key)
 #pragma unroll
                         for (int c = 0; c < D / 8; ++c) {
-                            const int bits = bad[buf][key][c] >> half * 4;
+                            const int bits = any_bad[buf][key >> 4] == now ? bad[buf][key][c] >> half * 4 : 0;
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 if (((bits >> r) & 1) && key < left)
@@ -847,13 +886,13 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
             }
             if (t + 1 < t1) {
                 stage_v(t + 1);
-                if (t + 2 < t1)
-                    load_k(t + 2);
-                if (t + 3 < t1)
-                    read_page(t + 3);
+                // past the end the last tile is read once more, and dropped
+                load_k(min(t + 2, t1 - 1));
+                read_page(min(t + 3, t1 - 1));
             }
             __syncthreads();
         }
+        number += max(t1 - t0, 0);
 
         l += __shfl_xor(l, 32);
         if (live) {
@@ -926,7 +965,7 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a, int token
     __shared__ f32x4 wave_o[kWaves][4][D / 4];
     const Sched &s = a.s;
     const Paged &p = s.p;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15, grp = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_of_thread(), sub = lane & 15, grp = lane >> 4;
     const int64_t slots = 2 * (int64_t)s.stream_wgs * s.stream_rows, plane = p.b.n_tokens * s.n_heads;
 
     const int64_t tok0 = (int64_t)blockIdx.x * tokens;
