@@ -20,6 +20,8 @@
 // attention_schedule.h says which kernel takes which rows and keys.
 #include <limits.h>
 
+#include <type_traits>
+
 #include "attention_schedule.h"
 #include "bd_device.h"
 #include "decoder_launch.h"
@@ -115,6 +117,9 @@ __device__ __forceinline__ float max_of_halves(float x)
     const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+
+// Waits for this wave's LDS accesses.
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -537,7 +542,7 @@ template <int D>
 struct TiledLds {
     __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * Stride<D>::k], vt[2][kTileKeys * Stride<D>::v];
     uint8_t key_held[2][kTileKeys], bad[2][kTileKeys][D / 8];
-    int hole[2][kWaves], any_bad[2][kWaves];
+    int hole[2][kWaves], any_bad[2][kWaves], holes;
     Scan scan, scan2;
     Located found;
     Groups groups;
@@ -548,6 +553,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
 {
     constexpr int KS = D / 16, DB = D / 32;
     constexpr int ES = E4M3 ? 1 : 2;
+    constexpr int NR = tile_rows(D) / (32 * kWaves);
     constexpr int NL = D * ES / 64;   // loads of a thread, K and V each: four threads a key, 64 bytes a load
     static_assert(kThreads == 4 * kTileKeys, "four threads a key");
     constexpr int KR = Stride<D>::k, VR = Stride<D>::v;
@@ -590,7 +596,10 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
 
     // Tiles are numbered over all items of the workgroup.  A wave that stages
     // keys without a cell, or values that are not finite, leaves the tile's
-    // number in its flag; nothing is written for the other tiles.
+    // number in its flag; nothing is written for the other tiles.  `holes` stays
+    // set from the first tile with such keys on.
+    if (threadIdx.x == 0)
+        sh.holes = 0;
     if (threadIdx.x < 2 * kWaves)
         (&hole[0][0])[threadIdx.x] = (&any_bad[0][0])[threadIdx.x] = -1;
     int number = 0;
@@ -613,8 +622,8 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         const int64_t idx2 = quotient(idx, p.n_kv), idx3 = quotient(idx2, splits);
         const int head = (int)(idx - idx2 * p.n_kv), split = (int)(idx2 - idx3 * splits);
         const int64_t rows = rows_of(s, g);
-        const int row0 = (int)(tiled_row_tiles(s, g) - 1 - idx3) * kTileRows;
-        const int rows_here = (int)min((int64_t)kTileRows, rows - row0);
+        const int row0 = (int)(tiled_row_tiles(s, g) - 1 - idx3) * tile_rows(D);
+        const int rows_here = (int)min((int64_t)tile_rows(D), rows - row0);
         const int pre_tiles = (int)cdiv(g.pre, kTileKeys);
         const bool is_prefix = seg >= p.b.n_seqs;
         // tiles up to the last row's own key; a split's share is that of the whole segment
@@ -624,37 +633,48 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         const int32_t *own_table = is_prefix ? nullptr : p.b.page_table + (int64_t)seg * p.b.max_pages;
         const int32_t *pre_table = g.pre ? p.b.prefix_table + (int64_t)g.group * p.b.max_prefix_pages : nullptr;
 
-        const int row = row0 + wave * 32 + col, tok = row / s.group;
-        const bool live = row < rows;
-        const int seen = live ? own_seen(g, tok) : 0;
-        const int wave_rows = rows_here - wave * 32;                       // may be negative
-        const int least = own_seen(g, (row0 + wave * 32) / s.group);       // the wave's first row
+        // the wave's rows: NR blocks of 32, a lane's row in block n is rowi[n]
+        int tok[NR], seen[NR];
+        int64_t cell_out[NR];
+        bf16x8 q[NR][KS];
+        const int wave_row = row0 + wave * 32 * NR, wave_rows = min(rows_here - wave * 32 * NR, 32 * NR);   // may be negative
+        const int least = own_seen(g, wave_row / s.group);               // own keys of the wave's first row: the fewest
         const int least_all = own_seen(g, row0 / s.group);
-        const int most = wave_rows <= 0 ? 0 : own_seen(g, (row0 + min(rows_here, wave * 32 + 32) - 1) / s.group);
-        const int64_t cell_out = (g.tok0 + (int64_t)tok) * s.n_heads + head * s.group + row - tok * s.group;
-        bf16x8 q[KS];
-        {
-            const uint16_t *src = a.q + (g.tok0 + (int64_t)tok) * a.q_stride +
-                                  (int64_t)(head * s.group + row - tok * s.group) * D + half * 8;
+        const int most = wave_rows <= 0 ? 0 : own_seen(g, (wave_row + wave_rows - 1) / s.group);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int row = wave_row + n * 32 + col;
+            const bool live = row < rows;
+            tok[n] = live ? row / s.group : -1;
+            const int h = live ? head * s.group + row - tok[n] * s.group : 0;
+            seen[n] = live ? own_seen(g, tok[n]) : 0;
+            cell_out[n] = (g.tok0 + (int64_t)tok[n]) * s.n_heads + h;
+            const uint16_t *from = a.q + (g.tok0 + (int64_t)max(tok[n], 0)) * a.q_stride + (int64_t)h * D + half * 8;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
-                q[k] = as_bf16x8(live ? *reinterpret_cast<const uint4 *>(src + k * 16) : make_uint4(0, 0, 0, 0));
+                q[n][k] = as_bf16x8(live ? *reinterpret_cast<const uint4 *>(from + k * 16) : make_uint4(0, 0, 0, 0));
         }
-        f32x16 o[DB];
-        float m = -INFINITY, l = 0.0f;
+        f32x16 o[NR][DB];
+        float m[NR], l[NR];
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+        for (int n = 0; n < NR; ++n) {
+            m[n] = -INFINITY, l[n] = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                o[d][r] = 0.0f;
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    o[n][d][r] = 0.0f;
+        }
         const float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
 
         // One set of registers carries K of the next tile until the scores of
         // this one are done, then its V.  A key without a cell reads cell 0: its
         // score is masked, its value cleared.
         int page = 0, cell = -1;
-        uint4 in[NL];
         const uint8_t *src = nullptr;
+        struct Loads {
+            uint4 at[NL];
+        } in;
         // Four threads a key, so a key's cell and address are formed once.  The
         // 16 keys of a wave are dealt so that 16 neighbouring threads, four keys,
         // write to different banks under both row strides.
@@ -668,7 +688,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         const auto load = [&](const uint8_t *from) {
 #pragma unroll
             for (int i = 0; i < NL; ++i)
-                in[i] = *reinterpret_cast<const uint4 *>(from + i * 64);
+                in.at[i] = *reinterpret_cast<const uint4 *>(from + i * 64);
         };
         const auto load_k = [&](int t) {
             const bool own = t >= pre_tiles;
@@ -684,41 +704,38 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         const int ldc = part * (E4M3 ? 2 : 1);                     // first of a load's 8-column pieces
         constexpr int PIECES = E4M3 ? 2 : 1, STEP = 4 * PIECES;
         const int num0 = number - t0;                              // tile t has number num0 + t
-        const auto stage_k = [&](int t) {
-            uint4 *dst = reinterpret_cast<uint4 *>(kt[t & 1] + ldr * KR + ldc * 8);
+        const auto put = [&](uint16_t *tile, int stride) {
+            uint4 *dst = reinterpret_cast<uint4 *>(tile + ldr * stride + ldc * 8);
 #pragma unroll
             for (int i = 0; i < NL; ++i)
                 if (E4M3) {
-                    dst[i * STEP] = e4m3x8_to_bf16(in[i].x, in[i].y);
-                    dst[i * STEP + 1] = e4m3x8_to_bf16(in[i].z, in[i].w);
+                    dst[i * STEP] = e4m3x8_to_bf16(in.at[i].x, in.at[i].y);
+                    dst[i * STEP + 1] = e4m3x8_to_bf16(in.at[i].z, in.at[i].w);
                 } else {
-                    dst[i * STEP] = in[i];
+                    dst[i * STEP] = in.at[i];
                 }
+        };
+        const auto stage_k = [&](int t) {
+            put(kt[t & 1], KR);
             if (__any(cell < 0)) {
                 key_held[t & 1][ldr] = cell >= 0;
                 hole[t & 1][wave] = num0 + t;
+                sh.holes = 1;
             }
         };
-        const auto stage_v = [&](int t) {
+        const auto stage_v = [&](int t, auto plain) {
             const int buf = t & 1;
-            uint4 *dst = reinterpret_cast<uint4 *>(vt[buf] + ldr * VR + ldc * 8);
-            if (!partial(t) && !__any(cell < 0)) {
-#pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    if (E4M3) {
-                        dst[i * STEP] = e4m3x8_to_bf16(in[i].x, in[i].y);
-                        dst[i * STEP + 1] = e4m3x8_to_bf16(in[i].z, in[i].w);
-                    } else {
-                        dst[i * STEP] = in[i];
-                    }
+            if ((decltype(plain)::value || !partial(t)) && !__any(cell < 0)) {
+                put(vt[buf], VR);
                 return;
             }
+            uint4 *dst = reinterpret_cast<uint4 *>(vt[buf] + ldr * VR + ldc * 8);
             uint32_t found_bad = 0;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
-                uint4 v[2] = {in[i], in[i]};
+                uint4 v[2] = {in.at[i], in.at[i]};
                 if (E4M3)
-                    v[0] = e4m3x8_to_bf16(in[i].x, in[i].y), v[1] = e4m3x8_to_bf16(in[i].z, in[i].w);
+                    v[0] = e4m3x8_to_bf16(in.at[i].x, in.at[i].y), v[1] = e4m3x8_to_bf16(in.at[i].z, in.at[i].w);
 #pragma unroll
                 for (int e = 0; e < PIECES; ++e) {
                     if (cell < 0)
@@ -737,32 +754,33 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         // q has to be there before the loop: its wait inside would be one for all loads in flight
         wait_vmcnt<0>();
         if (t0 < t1) {
+            // past the end the last tile is read once more, and dropped
             read_page(t0);
             load_k(t0);
             stage_k(t0);
             load(src);
-            if (t0 + 1 < t1)
-                read_page(t0 + 1);
-            stage_v(t0);
-            if (t0 + 1 < t1)
-                load_k(t0 + 1);
-            if (t0 + 2 < t1)
-                read_page(t0 + 2);
+            read_page(min(t0 + 1, t1 - 1));
+            stage_v(t0, std::false_type());
+            load_k(min(t0 + 1, t1 - 1));
+            read_page(min(t0 + 2, t1 - 1));
         }
         __syncthreads();
-        for (int t = t0; t < t1; ++t) {
-            const int buf = t & 1;
+        // One step.  A wave issues an instruction every 8 cycles at best and two
+        // waves share a SIMD, so what a step costs is its number of instructions;
+        // PLAIN steps, whose keys (and the next tile's) are in range and seen by
+        // all rows, leave out what only the others need, and reads are waited for
+        // by the group.
+        const auto step = [&](int t, auto plain) {
+            constexpr bool PLAIN = decltype(plain)::value;
+            const int buf = t & 1, now = num0 + t;
             const bool own = t >= pre_tiles;
             const int j0 = own ? (t - pre_tiles) * kTileKeys : 0;
-            const bool active = wave_rows > 0 && !(own && j0 >= most);
-            const int left = own ? seen - j0 : INT_MAX;
-            f32x16 x[2];
-            bool masked = false;
-            uint64_t held = 0;
+            const bool active = wave_rows > 0 && (PLAIN || !(own && j0 >= most)), more = PLAIN || t + 1 < t1;
+            f32x16 x[NR][2];
+            uint64_t held = ~0ull;
             if (active) {
-                // kAhead fragments are read ahead of the matrix instructions; the
-                // scheduling fences keep the compiler from drawing a read to its use
-                constexpr int kAhead = 6;
+                // the scheduling fences keep the compiler from drawing a read to its use
+                constexpr int kAhead = KS;
                 const uint16_t *kl = kt[buf] + col * KR + half * 8;
                 bf16x8 kf[kAhead];
                 const auto read_k = [&](int i) {
@@ -771,31 +789,39 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
                     read_k(i);
-                const int4 flags = *reinterpret_cast<const int4 *>(hole[buf]);
+                const int holes = sh.holes;
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        x[b][r] = 0.0f;
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            x[n][b][r] = 0.0f;
                 __builtin_amdgcn_s_setprio(1);
+                wait_lgkm0();
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < 2 * KS; ++i) {
-                    x[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % kAhead], q[i >> 1], x[i & 1], 0, 0, 0);
+                    if (i == kAhead)
+                        wait_lgkm0();
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        x[n][i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % kAhead], q[n][i >> 1], x[n][i & 1],
+                                                                              0, 0, 0);
                     if (i + kAhead < 2 * KS)
                         read_k(i + kAhead);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 __builtin_amdgcn_s_setprio(0);
-                held = ~0ull;
-                const int now = num0 + t;
-                if (flags.x == now || flags.y == now || flags.z == now || flags.w == now)
+                if (__builtin_amdgcn_readfirstlane(holes)) {
+                    const int4 flags = *reinterpret_cast<const int4 *>(hole[buf]);
                     held = __ballot(key_held[buf][lane] != 0) | (flags.x == now ? 0 : 0xFFFFull) |
                            (flags.y == now ? 0 : 0xFFFFull << 16) | (flags.z == now ? 0 : 0xFFFFull << 32) |
                            (flags.w == now ? 0 : 0xFFFFull << 48);
-                masked = held != ~0ull || (own && j0 + kTileKeys > least);
+                }
             }
-            if (t + 1 < t1) {
+            if (more) {
+                wait_vmcnt<1>();          // K of the next tile; the page number after it may still be on its way
                 stage_k(t + 1);
                 load(src);
             }
@@ -803,74 +829,97 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                 // keys 16 i + 4 half + 0..3 and + 8 of column 32 d + col
                 const uint16_t *vl = vt[buf] + (half * 4 + ((lane & 15) >> 2)) * VR + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
                 bf16x8 vf[2][DB];
-                const auto read_v = [&](int i) {
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const uint16_t *from = vl + i * 16 * VR + d * 32;
-                        const u32x2 lo = read_tr(from), hi = read_tr(from + 8 * VR);
-                        vf[i & 1][d] = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1]));
-                    }
+                const auto read_v = [&](int i, int d) {
+                    const uint16_t *from = vl + i * 16 * VR + d * 32;
+                    const u32x2 lo = read_tr(from), hi = read_tr(from + 8 * VR);
+                    vf[i & 1][d] = as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1]));
                 };
-                read_v(0);
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    read_v(0, d);
                 __builtin_amdgcn_sched_barrier(0);
-                if (masked) {
-                    const uint64_t ok = (held & first_bits64(left)) >> half * 4;
-                    const uint32_t word[2] = {(uint32_t)ok, (uint32_t)(ok >> 32)};
+                if (held != ~0ull || (!PLAIN && own && j0 + kTileKeys > least)) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const uint64_t ok = (held & first_bits64(own ? seen[n] - j0 : INT_MAX)) >> half * 4;
+                        const uint32_t word[2] = {(uint32_t)ok, (uint32_t)(ok >> 32)};
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                x[n][b][r] = (word[b] >> ((r >> 2) * 8 + (r & 3))) & 1u ? x[n][b][r] : -INFINITY;
+                    }
+                }
+                float mx[NR], mu[NR];
+                bool grown = false;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    mx[n] = -INFINITY;
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
-                            x[b][r] = (word[b] >> ((r >> 2) * 8 + (r & 3))) & 1u ? x[b][r] : -INFINITY;
+                            mx[n] = fmaxf(mx[n], x[n][b][r]);
+                    mx[n] = max_of_halves(mx[n]) * sc;
+                    grown |= mx[n] > m[n] + 8.0f;
                 }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        mx = fmaxf(mx, x[b][r]);
-                mx = max_of_halves(mx) * sc;
                 // the maximum follows only where it grew by more than 2^8: weights
                 // up to 2^8 are as exact, and most tiles need no rescaling
-                if (__any(mx > m + 8.0f)) {
-                    const float mn = fmaxf(m, mx), keep = mn == -INFINITY ? 1.0f : exp2_(m - mn);
-                    m = mn;
-                    l *= keep;
+                if (__any(grown)) {
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        o[d] *= keep;
+                    for (int n = 0; n < NR; ++n) {
+                        const float mn = fmaxf(m[n], mx[n]), keep = mn == -INFINITY ? 1.0f : exp2_(m[n] - mn);
+                        m[n] = mn;
+                        l[n] *= keep;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+                            o[n][d] *= keep;
+                    }
                 }
-                const float mu = m == -INFINITY ? 0.0f : m;
-                // the weights of the next 16 keys are formed between the matrix
-                // instructions of these
-                float e[8];
+                float e[NR][8];
+                bf16x8 pf[2][NR];
+                const auto weigh = [&](int i, int n, int r) {
+                    e[n][r] = exp2_(fmaf(x[n][i >> 1][(i & 1) * 8 + r], sc, -mu[n]));
+                };
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    e[r] = exp2_(fmaf(x[0][r], sc, -mu));
-                bf16x8 pf = weights(e, l);
+                for (int n = 0; n < NR; ++n) {
+                    mu[n] = m[n] == -INFINITY ? 0.0f : m[n];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        weigh(0, n, r);
+                    pf[0][n] = weights(e[n], l[n]);
+                }
+                // the weights of the next 16 keys are formed, and their values read,
+                // between the matrix instructions of these
+                constexpr int kSlots = NR * DB, kPer = 8 * NR / kSlots;
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (i < 3)
-                        read_v(i + 1);
+                    wait_lgkm0();
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i & 1][d], pf, o[d], 0, 0, 0);
+                    for (int c = 0; c < kSlots; ++c) {
+                        const int d = c / NR, n = c % NR;
+                        o[n][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[i & 1][d], pf[i & 1][n], o[n][d], 0, 0, 0);
                         if (i < 3) {
+                            if (n == 0)
+                                read_v(i + 1, d);
 #pragma unroll
-                            for (int r = d * (8 / DB); r < (d + 1) * (8 / DB); ++r)
-                                e[r] = exp2_(fmaf(x[(i + 1) >> 1][((i + 1) & 1) * 8 + r], sc, -mu));
+                            for (int w = c * kPer; w < (c + 1) * kPer; ++w)
+                                weigh(i + 1, w >> 3, w & 7);
+                            if ((c + 1) * kPer % 8 == 0)
+                                pf[(i + 1) & 1][(c + 1) * kPer / 8 - 1] =
+                                    weights(e[(c + 1) * kPer / 8 - 1], l[(c + 1) * kPer / 8 - 1]);
                             __builtin_amdgcn_sched_barrier(0);
                         }
                     }
-                    if (i < 3)
-                        pf = weights(e, l);
                 }
                 __builtin_amdgcn_s_setprio(0);
-                const int now = num0 + t;
                 bool some = false;
-                for (int w = 0; w < kWaves; ++w)
-                    some |= partial(t) && any_bad[buf][w] == now;
+                if (!PLAIN && partial(t))
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w)
+                        some |= any_bad[buf][w] == now;
                 if (some) {
 #pragma unroll 1
                     for (int key = 0; key < kTileKeys; ++key)
@@ -878,43 +927,58 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                         for (int c = 0; c < D / 8; ++c) {
                             const int bits = any_bad[buf][key >> 4] == now ? bad[buf][key][c] >> half * 4 : 0;
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (((bits >> r) & 1) && key < left)
-                                    o[c >> 2][(c & 3) * 4 + r] = NAN;
+                            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    if (((bits >> r) & 1) && key < seen[n] - j0)
+                                        o[n][c >> 2][(c & 3) * 4 + r] = NAN;
                         }
                 }
             }
-            if (t + 1 < t1) {
-                stage_v(t + 1);
-                // past the end the last tile is read once more, and dropped
-                load_k(min(t + 2, t1 - 1));
+            if (more) {
+                wait_vmcnt<0>();
+                stage_v(t + 1, plain);
+                load_k(PLAIN ? t + 2 : min(t + 2, t1 - 1));
                 read_page(min(t + 3, t1 - 1));
             }
             __syncthreads();
-        }
+        };
+        // plain tiles end with the last whole one that all rows see, and the last
+        // of the prefix is whole or not
+        const int whole_pre = g.pre / kTileKeys, whole_own = min(g.own, least_all) / kTileKeys;
+        const int plain_end = min(t1, pre_tiles > whole_pre && t0 < pre_tiles ? whole_pre : pre_tiles + whole_own) - 1;
+        int t = t0;
+        for (; t < plain_end - 1; ++t)
+            step(t, std::true_type());
+        for (; t < t1; ++t)
+            step(t, std::false_type());
         number += max(t1 - t0, 0);
 
-        l += __shfl_xor(l, 32);
-        if (live) {
-            const float vs = E4M3 && a.v_scale ? a.v_scale[head] : 1.0f;
-            const bool whole = splits == 1 && !g.shared;
-            const float f = whole ? (l == 0.0f ? 0.0f : vs / l) : vs;
-            const int64_t plane = is_prefix ? s.splits + split : split;
-            const int64_t pr = 2 * (int64_t)s.stream_wgs * s.stream_rows +
-                               plane * s.p.b.n_tokens * s.n_heads + cell_out;
+        const float vs = E4M3 && a.v_scale ? a.v_scale[head] : 1.0f;
+        const bool whole = splits == 1 && !g.shared;
+        const int64_t plane = is_prefix ? s.splits + split : split;
+        const int64_t plane_row = 2 * (int64_t)s.stream_wgs * s.stream_rows + plane * s.p.b.n_tokens * s.n_heads;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            l[n] += __shfl_xor(l[n], 32);
+            if (tok[n] < 0)
+                continue;
+            const float f = whole ? (l[n] == 0.0f ? 0.0f : vs / l[n]) : vs;
+            const int64_t pr = plane_row + cell_out[n];
             if (!whole && half == 0)
-                a.part_ml[pr] = make_float2(m, l);
+                a.part_ml[pr] = make_float2(m[n], l[n]);
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int c = d * 32 + r * 8 + half * 4;
-                    const f32x4 w = {o[d][4 * r] * f, o[d][4 * r + 1] * f, o[d][4 * r + 2] * f, o[d][4 * r + 3] * f};
+                    const f32x4 w = {o[n][d][4 * r] * f, o[n][d][4 * r + 1] * f, o[n][d][4 * r + 2] * f,
+                                     o[n][d][4 * r + 3] * f};
                     if (whole) {
                         u32x2 b;
                         b[0] = pack_bf16x2(w[0], w[1]);
                         b[1] = pack_bf16x2(w[2], w[3]);
-                        *reinterpret_cast<u32x2 *>(a.out + cell_out * D + c) = b;
+                        *reinterpret_cast<u32x2 *>(a.out + cell_out[n] * D + c) = b;
                     } else {
                         *reinterpret_cast<f32x4 *>(a.part_o + pr * D + c) = w;
                     }
@@ -1134,14 +1198,15 @@ Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
     s.stream_rows = most <= 16 ? 16 : 32;
     s.few = s.tiled ? 32 : INT_MAX;
     s.stream_wgs = s.tiled ? 256 : 512;
+    s.tile_rows = tile_rows(c.head_dim);
     // enough splits that row tiles x key heads x splits fill the chip twice
-    const int64_t tiles = cdiv(T * s.group, kTileRows) * c.n_kv_heads;
+    const int64_t tiles = cdiv(T * s.group, s.tile_rows) * c.n_kv_heads;
     const int64_t want = cdiv(2 * kTiledSlots, tiles);
     s.splits = s.tiled ? (int32_t)(want < 1 ? 1 : want > 64 ? 64 : want) : 1;
     const int64_t planes = b.n_groups > 0 ? 2 * s.splits : s.splits > 1 ? s.splits : 0;
     pl.rows = 2 * (int64_t)s.stream_wgs * s.stream_rows + planes * T * n_heads;
     // a workgroup per item; where items are split they are few, and the bound is loose
-    const int64_t full = T * s.group / kTileRows;
+    const int64_t full = T * s.group / s.tile_rows;
     const int64_t row_tiles = full + (b.n_seqs < T ? b.n_seqs : T) + (b.n_groups > 0 ? full + b.n_groups : 0);
     const int64_t items = row_tiles * c.n_kv_heads * s.splits, cap = s.splits > 1 ? 2 * kTiledSlots : INT_MAX;
     const int64_t tiled_wgs = items < s.stream_wgs ? s.stream_wgs : items < cap ? items : cap;

@@ -25,7 +25,10 @@ namespace bd {
 
 constexpr int kStreamKeys = 32;      // keys of a streaming unit
 constexpr int kTileKeys = 64;        // keys of a tiled step
-constexpr int kTileRows = 128;       // rows of a tiled item
+// Rows of a tiled item: 32 a wave at 128 columns, 64 at 64, where their sums
+// fit beside a second wave's on the SIMD and every fragment read from LDS
+// serves twice the matrix work.
+constexpr int tile_rows(int head_dim) { return head_dim == 64 ? 256 : 128; }
 constexpr int kRunCost = 4;          // units that a run's beginning and end cost
 constexpr int kMinUnits = 4;         // units that are worth a workgroup: one a wave
 constexpr int kMinTiles = 4;         // key tiles that are worth a split
@@ -39,6 +42,7 @@ struct Sched {
     int32_t few;                     // rows up to which a sequence is streamed (INT32_MAX: all)
     int32_t stream_rows;             // rows of a streaming tile
     int32_t stream_wgs;              // workgroups of the streaming kernel
+    int32_t tile_rows;               // rows of a tiled item
     int32_t splits;                  // bound of a segment's splits
     bool tiled;                      // the tiled kernel runs
 };
@@ -126,7 +130,7 @@ BD_HD Segment tiled_segment(const Sched &s, const Groups &gr, int i)
         g.ntok = 0;
     return g;
 }
-BD_HD int64_t tiled_row_tiles(const Sched &s, const Segment &g) { return cdiv(rows_of(s, g), kTileRows); }
+BD_HD int64_t tiled_row_tiles(const Sched &s, const Segment &g) { return cdiv(rows_of(s, g), s.tile_rows); }
 // Work of a segment in key tiles (a causal one's as if it were not).
 BD_HD int64_t tiled_work(const Sched &s, const Segment &g)
 {

@@ -83,6 +83,7 @@ static Case make(std::mt19937 &r, bool sane)
     c.s.few = c.s.tiled ? 32 : INT_MAX;
     c.s.stream_rows = u(0, 1) ? 16 : 32;
     c.s.stream_wgs = u(0, 2) ? u(1, 40) : 512;
+    c.s.tile_rows = tile_rows(u(0, 1) ? 64 : 128);
     c.s.splits = c.s.tiled ? u(1, 9) : 1;
     return c;
 }
@@ -189,8 +190,8 @@ int main()
             for (int64_t idx = 0; idx < items; ++idx) {
                 const int splits = tiled_splits(s, g, depth), head = (int)(idx % p.n_kv);
                 const int split = (int)(idx / p.n_kv % splits);
-                const int64_t row0 = (tiled_row_tiles(s, g) - 1 - idx / p.n_kv / splits) * kTileRows;
-                const int64_t rows = std::min<int64_t>(kTileRows, rows_of(s, g) - row0);
+                const int64_t row0 = (tiled_row_tiles(s, g) - 1 - idx / p.n_kv / splits) * s.tile_rows;
+                const int64_t rows = std::min<int64_t>(s.tile_rows, rows_of(s, g) - row0);
                 EXPECT(row0 >= 0 && rows > 0);
                 const bool is_prefix = seg >= p.b.n_seqs;
                 const int last = is_prefix ? 0 : own_seen(g, (int)((row0 + rows - 1) / s.group));
