@@ -208,18 +208,24 @@ __device__ __forceinline__ void fill_groups(const Sched &s, Groups &gr)
 struct Located {
     int first;        // a segment at or before the one that holds the position
     int64_t base;     // where `first` begins
+    Segment segment;  // segment `first`, as its thread read it
 };
-template <typename Size>
+template <typename Read, typename Size>
 struct Listing {
     int n, per;
     int64_t mine, before, total;
-    __device__ __forceinline__ Listing(int n_, const Size &size, Scan &sh)
+    Segment head;     // the thread's first segment
+    __device__ __forceinline__ Listing(int n_, const Read &read, const Size &size, Scan &sh)
     {
         n = n_, per = (n + kThreads - 1) / kThreads;
         mine = 0;
         const int i0 = threadIdx.x * per;
-        for (int i = i0; i < min(n, i0 + per); ++i)
-            mine += size(i);
+        for (int i = i0; i < min(n, i0 + per); ++i) {
+            const Segment g = read(i);
+            if (i == i0)
+                head = g;
+            mine += size(g);
+        }
         before = scan_block(mine, sh, total);
     }
     // position in [0, total), the same in all threads
@@ -227,7 +233,7 @@ struct Listing {
     {
         __syncthreads();
         if (before <= position && position < before + mine)
-            *sh = {(int)threadIdx.x * per, before};
+            *sh = {(int)threadIdx.x * per, before, head};
         __syncthreads();
         return *sh;
     }
@@ -241,6 +247,9 @@ struct Listing {
 // piece of LDS; no barrier until the workgroup's run of one key head ends and
 // the four waves' states are joined.  Eight waves a CU with 16 KB each on the
 // way cover the memory latency.
+// Workgroups of it that fit a CU, by their registers.
+constexpr int stream_per_cu(int d, bool e4m3, int nb) { return nb == 1 && (e4m3 || d == 64) ? 3 : 2; }
+
 template <int D, int NB>
 struct StreamLds {
     static constexpr int kJoin = kWaves * 16 * NB * (D + 4) * 4, kStage = kWaves * kStreamKeys * Stride<D>::v_stream * 2;
@@ -270,8 +279,9 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
     const Paged &p = s.p;
     const int lane = threadIdx.x & 63, wave = wave_of_thread(), col = lane & 15, quad = lane >> 4;
     fill_groups(s, groups);
-    const auto size = [&](int i) { return stream_units(s, sequence(s, groups, i)); };
-    const Listing list(p.b.n_seqs, size, sh.scan);
+    const auto read = [&](int i) { return sequence(s, groups, i); };
+    const auto size = [&](const Segment &g) { return stream_units(s, g); };
+    const Listing list(p.b.n_seqs, read, size, sh.scan);
     const int64_t chunk = stream_chunk(s, list.total);
     int64_t at = block * chunk;
     const int64_t end = min(list.total, at + chunk);
@@ -281,7 +291,7 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
         int64_t b = list.before;
         for (int i = threadIdx.x * list.per; i < min(list.n, (int)(threadIdx.x + 1) * list.per); ++i) {
             a.cut[2 + i] = b;
-            b += list.per > 1 ? size(i) : 0;
+            b += list.per > 1 ? size(read(i)) : 0;
         }
     }
     if (at >= end)
@@ -289,14 +299,14 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
     const Located loc = list.locate(at, &sh.found);
     int seq = loc.first;
     int64_t base = loc.base;
-    Segment g = sequence(s, groups, seq);
+    Segment g = loc.segment;
     uint16_t *vt = reinterpret_cast<uint16_t *>(sh.tiles) + wave * kStreamKeys * VS;
     float *oj = reinterpret_cast<float *>(sh.tiles);
 
     while (at < end) {
         for (int64_t units; base + (units = stream_units(s, g)) <= at;) {
             base += units;
-            g = sequence(s, groups, ++seq);
+            g = read(++seq);
         }
         const int tiles = key_tiles(g, kStreamKeys), pre_tiles = (int)cdiv(g.pre, kStreamKeys);
         const int64_t row_tiles = stream_row_tiles(s, g), rows = rows_of(s, g);
@@ -591,8 +601,9 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
     }
     if (block == 0 && threadIdx.x == 0)
         a.cut[0] = depth;
-    const auto size = [&](int i) { return tiled_items(s, tiled_segment(s, groups, i), depth); };
-    const Listing<decltype(size)> list(n_seg, size, sh.scan);
+    const auto read = [&](int i) { return tiled_segment(s, groups, i); };
+    const auto size = [&](const Segment &g) { return tiled_items(s, g, depth); };
+    const Listing list(n_seg, read, size, sh.scan);
 
     // Tiles are numbered over all items of the workgroup.  A wave that stages
     // keys without a cell, or values that are not finite, leaves the tile's
@@ -608,13 +619,10 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         const Located loc = list.locate(item, &sh.found);
         int seg = loc.first;
         int64_t base = loc.base;
-        Segment g;
-        for (;; ++seg) {
-            g = tiled_segment(s, groups, seg);
-            const int64_t n = tiled_items(s, g, depth);
-            if (item < base + n)
-                break;
+        Segment g = loc.segment;
+        for (int64_t n; item >= base + (n = size(g));) {
             base += n;
+            g = read(++seg);
         }
         // heads fastest, then splits, then row tiles from the last (the longest) to the first
         const int64_t idx = item - base;
@@ -990,7 +998,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
 // ---------------------------------------------------------------------- kernels
 
 template <int D, bool E4M3, int NB>
-__global__ __launch_bounds__(kThreads, 2) void attention_stream(AttnArgs a)
+__global__ __launch_bounds__(kThreads, stream_per_cu(D, E4M3, NB)) void attention_stream(AttnArgs a)
 {
     __shared__ StreamLds<D, NB> sh;
     stream_body<D, E4M3, NB>(a, sh, blockIdx.x);
@@ -1197,7 +1205,7 @@ Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
     s.tiled = b.n_groups > 0 || most > 32;
     s.stream_rows = most <= 16 ? 16 : 32;
     s.few = s.tiled ? 32 : INT_MAX;
-    s.stream_wgs = s.tiled ? 256 : 512;
+    s.stream_wgs = 256 * (s.tiled ? 1 : stream_per_cu(c.head_dim, c.dtype == BD_KV_E4M3, s.stream_rows / 16));
     s.tile_rows = tile_rows(c.head_dim);
     // enough splits that row tiles x key heads x splits fill the chip twice
     const int64_t tiles = cdiv(T * s.group, s.tile_rows) * c.n_kv_heads;

@@ -14,104 +14,120 @@
 namespace bd {
 namespace {
 
-// Eight consecutive elements, of which n (1..8) exist.  Global memory takes
-// 16-byte accesses at any element alignment, so one form serves odd widths
-// and strides too.
+// Eight consecutive elements as loaded, of which n (1..8) exist, the others
+// zero.  Global memory takes 16-byte accesses at any element alignment, so one
+// form serves odd widths and strides too.
 typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
 
-__device__ __forceinline__ void load8(const uint16_t *p, int n, float *f)
-{
-    if (n == 8) {
-        const u32x4a2 w = *reinterpret_cast<const u32x4a2 *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = lo_f32(w[i]);
-            f[2 * i + 1] = hi_f32(w[i]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[i] = i < n ? lo_f32(p[i]) : 0.0f;
-}
+template <typename T>
+struct Eight;
 
-__device__ __forceinline__ void load8(const float *p, int n, float *f)
-{
-    if (n == 8) {
-        const u32x4a4 a = *reinterpret_cast<const u32x4a4 *>(p), b = *reinterpret_cast<const u32x4a4 *>(p + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = __uint_as_float(a[i]);
-            f[4 + i] = __uint_as_float(b[i]);
+template <>
+struct Eight<uint16_t> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const uint16_t *p, int n)
+    {
+        if (n == 8) {
+            w = *reinterpret_cast<const u32x4a2 *>(p);
+            return;
         }
-        return;
-    }
+        w = (u32x4){0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[i] = i < n ? p[i] : 0.0f;
-}
-
-__device__ __forceinline__ void store8(uint16_t *p, int n, const float *f)
-{
-    if (n == 8) {
-        u32x4a2 w;
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    }
+    __device__ __forceinline__ float get(int i) const { return i & 1 ? hi_f32(w[i >> 1]) : lo_f32(w[i >> 1]); }
+    __device__ __forceinline__ void set(const float *f)
+    {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-        *reinterpret_cast<u32x4a2 *>(p) = w;
-        return;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n)
-            p[i] = to_bf16(f[i]);
-}
-
-__device__ __forceinline__ void store8(float *p, int n, const float *f)
-{
-    if (n == 8) {
-        u32x4a4 a, b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = __float_as_uint(f[i]);
-            b[i] = __float_as_uint(f[4 + i]);
+    __device__ __forceinline__ void store(uint16_t *p, int n) const
+    {
+        if (n == 8) {
+            *reinterpret_cast<u32x4a2 *>(p) = w;
+            return;
         }
-        *reinterpret_cast<u32x4a4 *>(p) = a;
-        *reinterpret_cast<u32x4a4 *>(p + 4) = b;
-        return;
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n)
-            p[i] = f[i];
-}
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+};
+
+template <>
+struct Eight<float> {
+    float f[8];
+    __device__ __forceinline__ void load(const float *p, int n)
+    {
+        if (n == 8) {
+            const u32x4 a = *reinterpret_cast<const u32x4a4 *>(p), b = *reinterpret_cast<const u32x4a4 *>(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[i] = __uint_as_float(a[i]), f[4 + i] = __uint_as_float(b[i]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = i < n ? p[i] : 0.0f;
+    }
+    __device__ __forceinline__ float get(int i) const { return f[i]; }
+    __device__ __forceinline__ void set(const float *g)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = g[i];
+    }
+    __device__ __forceinline__ void store(float *p, int n) const
+    {
+        if (n == 8) {
+            u32x4 a, b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[i] = __float_as_uint(f[i]), b[i] = __float_as_uint(f[4 + i]);
+            *reinterpret_cast<u32x4a4 *>(p) = a;
+            *reinterpret_cast<u32x4a4 *>(p + 4) = b;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                p[i] = f[i];
+    }
+};
 
 // Sum over the workgroup; every thread gets it.  `part` holds one float a wave.
-template <int T>
 __device__ __forceinline__ float sum_all(float v, float *part)
 {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
         v += __shfl_xor(v, o);
-    if (T == 64)
+    const int waves = blockDim.x >> 6;
+    if (waves == 1)
         return v;
     if ((threadIdx.x & 63) == 0)
         part[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.0f;
+    // each wave sums the parts for itself
+    const int lane = threadIdx.x & 63;
+    v = lane < waves ? part[lane] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < T / 64; ++i)
-        v += part[i];
-    return v;
+    for (int o = 8; o > 0; o >>= 1)
+        v += __shfl_xor(v, o);
+    return __shfl(v, 0);
 }
 
-template <int T, int C, typename RT, typename WT>
-__global__ __launch_bounds__(T) void block_norm_rows(NormArgs a)
+// C groups of eight columns a thread.  Inputs stay as loaded until they are
+// used (half the registers for bf16), so that 32 waves fit a CU.
+template <int C, typename RT, typename WT>
+__global__ __launch_bounds__(1024, C == 1 ? 8 : 4) void block_norm_rows(NormArgs a)
 {
-    __shared__ float part[2][T / 64];
+    __shared__ float part[2][16];
     const int64_t i = blockIdx.x;
-    const int d = a.d;
+    const int d = a.d, T = blockDim.x;
     const int v = a.ids ? a.ids[i] : 0;
     const bool known = (unsigned)v < (unsigned)a.n_variants;
     const RT *res = static_cast<const RT *>(a.residual) + i * a.residual_stride;
@@ -119,98 +135,97 @@ __global__ __launch_bounds__(T) void block_norm_rows(NormArgs a)
     const bool wants_x = a.pre_weight != nullptr, pre = wants_x && known;
     const int64_t wrow = known ? (int64_t)v * d : 0;
 
-    float r[C][8], b[C][8], g[C][8], wo[C][8], wi[C][8];
+    Eight<RT> r[C];
+    Eight<uint16_t> b[C], g[C];
+    Eight<WT> wo[C], wi[C];
     int n[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int at = (c * T + (int)threadIdx.x) * 8;
         n[c] = min(max(d - at, 0), 8);
         if (n[c] > 0) {
-            load8(res + at, n[c], r[c]);
+            r[c].load(res + at, n[c]);
             if (blk)
-                load8(a.block + i * a.block_stride + at, n[c], b[c]);
+                b[c].load(a.block + i * a.block_stride + at, n[c]);
             if (gated)
-                load8(a.gate + i * a.gate_stride + at, n[c], g[c]);
+                g[c].load(a.gate + i * a.gate_stride + at, n[c]);
             if (posted)
-                load8(static_cast<const WT *>(a.post_weight) + wrow + at, n[c], wo[c]);
+                wo[c].load(static_cast<const WT *>(a.post_weight) + wrow + at, n[c]);
             if (pre)
-                load8(static_cast<const WT *>(a.pre_weight) + wrow + at, n[c], wi[c]);
+                wi[c].load(static_cast<const WT *>(a.pre_weight) + wrow + at, n[c]);
         }
     }
-    if (blk) {
-        float k = a.scale;
-        if (posted) {
-            float s = 0.0f;
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (n[c] > 0)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        s = fmaf(b[c][j], b[c][j], s);
-            k *= 1.0f / sqrtf(sum_all<T>(s, part[0]) / (float)d + a.eps);
-        }
+    float k = a.scale;
+    if (posted) {
+        float s = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (n[c] > 0)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float y = b[c][j] * k;
+                for (int j = 0; j < 8; ++j)
+                    s = fmaf(b[c].get(j), b[c].get(j), s);
+        k *= 1.0f / sqrtf(sum_all(s, part[0]) / (float)d + a.eps);
+    }
+    float s = 0.0f, x[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (n[c] > 0) {
+            const int at = (c * T + (int)threadIdx.x) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[c][j] = r[c].get(j);
+                if (blk) {
+                    float y = b[c].get(j) * k;
                     if (posted)
-                        y *= wo[c][j];
+                        y *= wo[c].get(j);
                     if (gated) {
-                        const float z = g[c][j];
+                        const float z = g[c].get(j);
                         // exp(-z) past the range gives sigmoid 0 (and silu -0) as it should
                         const float sig = 1.0f / (1.0f + __expf(-z));
                         y *= a.gate_act == BD_GATE_NONE ? z : a.gate_act == BD_GATE_SIGMOID ? sig : z * sig;
                     }
-                    r[c][j] += y;
+                    x[c][j] += y;
                 }
-    }
-    if (a.residual_out) {
-        RT *out = static_cast<RT *>(a.residual_out) + i * a.out_stride;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (n[c] > 0)
-                store8(out + (c * T + (int)threadIdx.x) * 8, n[c], r[c]);
-    }
+                // columns past the row's end are zero, also with a gate (their block is)
+                s = fmaf(x[c][j], x[c][j], s);
+            }
+            if (a.residual_out) {
+                Eight<RT> out;
+                out.set(x[c]);
+                out.store(static_cast<RT *>(a.residual_out) + i * a.out_stride + at, n[c]);
+            }
+        }
     if (!wants_x)
         return;
-    float k = 0.0f;
-    if (pre) {
-        float s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n[c])
-                    s = fmaf(r[c][j], r[c][j], s);
-        k = 1.0f / sqrtf(sum_all<T>(s, part[1]) / (float)d + a.eps);
-    }
+    k = pre ? 1.0f / sqrtf(sum_all(s, part[1]) / (float)d + a.eps) : 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
         if (n[c] > 0) {
-            float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                x[j] = pre ? r[c][j] * k * wi[c][j] : 0.0f;
-            store8(a.x + i * (int64_t)d + (c * T + (int)threadIdx.x) * 8, n[c], x);
+                x[c][j] = pre ? x[c][j] * k * wi[c].get(j) : 0.0f;
+            Eight<uint16_t> out;
+            out.set(x[c]);
+            out.store(a.x + i * (int64_t)d + (c * T + (int)threadIdx.x) * 8, n[c]);
         }
 }
 
-template <int T, int C>
+template <int C>
 void start(const NormArgs &a, hipStream_t s)
 {
+    // as many waves as the row has groups of 512 columns
+    const int threads = (a.d + 512 * C - 1) / (512 * C) * 64;
     const dim3 grid((unsigned)a.m);
     if (a.residual_f32) {
         if (a.weight_f32)
-            block_norm_rows<T, C, float, float><<<grid, T, 0, s>>>(a);
+            block_norm_rows<C, float, float><<<grid, threads, 0, s>>>(a);
         else
-            block_norm_rows<T, C, float, uint16_t><<<grid, T, 0, s>>>(a);
+            block_norm_rows<C, float, uint16_t><<<grid, threads, 0, s>>>(a);
     } else {
         if (a.weight_f32)
-            block_norm_rows<T, C, uint16_t, float><<<grid, T, 0, s>>>(a);
+            block_norm_rows<C, uint16_t, float><<<grid, threads, 0, s>>>(a);
         else
-            block_norm_rows<T, C, uint16_t, uint16_t><<<grid, T, 0, s>>>(a);
+            block_norm_rows<C, uint16_t, uint16_t><<<grid, threads, 0, s>>>(a);
     }
 }
 
@@ -218,16 +233,14 @@ void start(const NormArgs &a, hipStream_t s)
 
 hipError_t launch_block_norm(const NormArgs &a, hipStream_t s)
 {
-    if (a.d <= 512)
-        start<64, 1>(a, s);
-    else if (a.d <= 2048)
-        start<256, 1>(a, s);
-    else if (a.d <= 8192)
-        start<1024, 1>(a, s);
+    // two groups a thread: half the waves to add up (4096 x 8192 bf16: 65 -> 55 us,
+    // 4099 x 8192 fp32, gated: 103 -> 98 us); one where a row is a few waves
+    if (a.d <= 2048)
+        start<1>(a, s);
     else if (a.d <= 16384)
-        start<1024, 2>(a, s);
+        start<2>(a, s);
     else
-        start<1024, 4>(a, s);
+        start<4>(a, s);
     return hipGetLastError();
 }
 
