@@ -305,8 +305,10 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
 
     while (at < end) {
         for (int64_t units; base + (units = stream_units(s, g)) <= at;) {
+            if (++seq >= p.b.n_seqs)
+                return;      // only where the lengths changed under the call
             base += units;
-            g = read(++seq);
+            g = read(seq);
         }
         const int tiles = key_tiles(g, kStreamKeys), pre_tiles = (int)cdiv(g.pre, kStreamKeys);
         const int64_t row_tiles = stream_row_tiles(s, g), rows = rows_of(s, g);
@@ -621,8 +623,10 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         int64_t base = loc.base;
         Segment g = loc.segment;
         for (int64_t n; item >= base + (n = size(g));) {
+            if (++seg >= n_seg)
+                return;      // only where the lengths changed under the call
             base += n;
-            g = read(++seg);
+            g = read(seg);
         }
         // heads fastest, then splits, then row tiles from the last (the longest) to the first
         const int64_t idx = item - base;
@@ -876,8 +880,10 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                 if (__any(grown)) {
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
-                        const float mn = fmaxf(m[n], mx[n]), keep = mn == -INFINITY ? 1.0f : exp2_(m[n] - mn);
-                        m[n] = mn;
+                        // row by row, so that no row's bits depend on another's scores
+                        const bool follows = mx[n] > m[n] + 8.0f;
+                        const float keep = follows ? exp2_(m[n] - mx[n]) : 1.0f;
+                        m[n] = follows ? mx[n] : m[n];
                         l[n] *= keep;
 #pragma unroll
                         for (int d = 0; d < DB; ++d)

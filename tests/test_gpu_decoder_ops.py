@@ -251,11 +251,12 @@ def test_attention_rows_without_keys(bd):
     assert bd.attention(c.q[:0], c.kv(bd), b).shape == (0, 8, 64)
 
 
-@pytest.mark.parametrize("new", [[1, 2, 1], [50, 2, 33]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [[1, 2, 1], [50, 2, 33], [150, 20, 70]])
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
-def test_attention_bad_pages_lengths_and_starts(bd, new, cache):
+def test_attention_bad_pages_lengths_and_starts(bd, new, cache, D):
     """Page numbers out of range hold no key, lengths end with the table, starts with the tokens."""
-    c = Case(new, [100, 40, 77], 8, 2, 128, 16, cache, groups=[(0, 3, 90)], seed=4)
+    c = Case(new, [100, 40, 77], 8, 2, D, 16, cache, groups=[(0, 3, 90)], seed=4)
     c.host.table[0, 2], c.host.table[1, 0], c.host.table[2, 1] = -1, c.n_pages, 2 ** 31 - 1
     c.host.ptable[0, [0, 3]] = -2 ** 31, c.n_pages + 5
     c.check(bd)
@@ -275,11 +276,12 @@ def test_attention_bad_pages_lengths_and_starts(bd, new, cache):
     assert torch.equal(bd.attention(c.q, c.kv(bd), c2), bd.attention(c.q, c.kv(bd), c3))
 
 
-@pytest.mark.parametrize("new,ctx", [([2, 3], [20, 40]), ([70, 3], [9, 40])])
-def test_attention_later_keys_do_not_reach_earlier_rows(bd, new, ctx):
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,ctx", [([2, 3], [20, 40]), ([70, 3], [9, 40]), ([200, 3], [190, 40])])
+def test_attention_later_keys_do_not_reach_earlier_rows(bd, new, ctx, D):
     """NaN and infinities in a key or value show in the tokens that see it and in no other."""
     for which, bad in (("k", NAN), ("v", NAN), ("v", float("inf")), ("v", -float("inf")), ("k", float("inf"))):
-        c = Case(new, ctx, 8, 2, 128, 16, seed=6)
+        c = Case(new, ctx, 8, 2, D, 16, seed=6)
         want = bd.attention(c.q, c.kv(bd), c.batch(bd)).clone()
         at = ctx[0] + new[0] - 1                        # the last token's own cell
         pg = int(c.host.table[0, at // 16])
@@ -291,7 +293,7 @@ def test_attention_later_keys_do_not_reach_earlier_rows(bd, new, ctx):
         assert torch.equal(got[new[0] - 1, 4:], want[new[0] - 1, 4:])
         if which == "v":
             assert not got[new[0] - 1, :4, 5].isfinite().any()
-            rest = [i for i in range(128) if i != 5]
+            rest = [i for i in range(D) if i != 5]
             assert torch.equal(got[new[0] - 1, :4, rest], want[new[0] - 1, :4, rest])
 
 
@@ -300,6 +302,16 @@ def test_attention_large_scores(bd):
     c = Case([1, 40], [700, 100], 8, 2, 128, 16, seed=8)
     c.check(bd, scale=40.0)
     c.check(bd, scale=1e-6)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_attention_long_prompt_and_context(bd, cache):
+    """Many plain steps, splits of one sequence's keys, and a bad page in the middle of them."""
+    c = Case([3, 140], [700, 1900], 4, 1, 128, 32, cache, seed=31)
+    c.host.table[1, 20] = -1
+    c.check(bd)
+    c = Case([260], [1500], 3, 1, 64, 64, cache, groups=[(0, 1, 500)], seed=32)
+    c.check(bd)
 
 
 def test_attention_strided_q_and_out(bd):
