@@ -246,7 +246,10 @@ struct Listing {
 // matrix instruction takes, V by whole rows and on through the wave's own
 // piece of LDS; no barrier until the workgroup's run of one key head ends and
 // the four waves' states are joined.  Eight waves a CU with 16 KB each on the
-// way cover the memory latency.
+// way cover the memory latency (twelve with 8 KB of an 8-bit cache).  64 users
+// with up to 16000 keys each, 64 query heads over 8 of 128: 380 us, 5.6 TB/s;
+// one user's 200003 keys 152 us, 5.4 TB/s; 96 users on an 8-bit cache 95 us,
+// 4.7 TB/s; one user's 1531 keys 9 us: four memory latencies and a launch.
 // Workgroups of it that fit a CU, by their registers.
 constexpr int stream_per_cu(int d, bool e4m3, int nb) { return nb == 1 && (e4m3 || d == 64) ? 3 : 2; }
 
@@ -547,9 +550,18 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
 // ------------------------------------------------------------- many rows: tiles
 //
 // Prompts and shared prefixes: matrix bound.  A workgroup holds 128 rows, 32
-// a wave, and walks 64-key tiles of K and V that all four waves read from LDS;
-// a tile's loads are in registers one step ahead, and LDS holds two tiles, so
-// a step has one barrier.
+// a wave (256 and 64 at 64 columns), and walks 64-key tiles of K and V that all
+// four waves read from LDS; a tile's loads are in registers one step ahead, and
+// LDS holds two tiles, so a step has one barrier.  Prompts of up to 4097 tokens,
+// 64 heads over 8 of 128: 420 us, 818 TFLOP/s of the causal work (a large bf16
+// product reaches 1398 here).  The matrix units are busy 35-40% of the cycles
+// at 2.0 GHz and so is the vector unit: leaving out all exponentials saves 5%,
+// three quarters of the second product 10%, any one kind of LDS read 2-4%, so
+// what bounds a step is a wave's own chain of about 300 instructions at 8
+// cycles each, two waves a SIMD (a third has no registers).  Measured and
+// dropped: eight waves that share a tile, also half a step apart (430 us), 64
+// rows a wave at 128 columns, one wave a SIMD (640 us), K fragments read ahead
+// over the barrier (435 us).
 template <int D>
 struct TiledLds {
     __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * Stride<D>::k], vt[2][kTileKeys * Stride<D>::v];
@@ -1012,7 +1024,8 @@ __global__ __launch_bounds__(kThreads, stream_per_cu(D, E4M3, NB)) void attentio
 
 // Both at once where a call may have work for both: the streaming workgroups
 // come first, one for each CU, and the tiled ones fill the other half, so that
-// the one's loads run under the other's matrix instructions.
+// the one's loads run under the other's matrix instructions (128 users behind
+// three prefixes: 74 us in two launches, 67 in one).
 template <int D, bool E4M3, int NB>
 __global__ __launch_bounds__(kThreads, 2) void attention_mixed(AttnArgs a)
 {
@@ -1033,7 +1046,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_mixed(AttnArgs a)
 // tokens that see nothing; finished rows are left alone.  Latency bound: 16
 // lanes take a head, so a wave has four heads' states on the way, and where
 // BY_PARTS (few tokens, perhaps many states a head) the four waves share the
-// states of the same four heads.
+// states of the same four heads: 6 us for one token's 64 heads of 13 states
+// each, 11 us of 64 (one wave a head and state after state: 10 and 35 us).
 template <int D, bool BY_PARTS>
 __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a, int tokens)
 {

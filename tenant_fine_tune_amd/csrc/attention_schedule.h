@@ -29,7 +29,8 @@ constexpr int kTileKeys = 64;        // keys of a tiled step
 // fit beside a second wave's on the SIMD and every fragment read from LDS
 // serves twice the matrix work.
 constexpr int tile_rows(int head_dim) { return head_dim == 64 ? 256 : 128; }
-constexpr int kRunCost = 4;          // units that a run's beginning and end cost
+constexpr int kRunCost = 4;          // units that a run's beginning and end cost (0: 75 us for 128 short
+                                     // contexts of 64 query heads, a workgroup then got up to 17 runs; 4: 33 us)
 constexpr int kMinUnits = 4;         // units that are worth a workgroup: one a wave
 constexpr int kMinTiles = 4;         // key tiles that are worth a split
 constexpr int kItemCost = 5;         // key tiles that a tiled item's beginning and end cost

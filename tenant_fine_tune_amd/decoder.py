@@ -65,6 +65,11 @@ def _dense(t, dtype, name, shape, dev):
     _refuse(t, dtype, name, shape, dev)
 
 
+def _like(t):
+    """A contiguous tensor of t's shape and type (options cost as much as the allocation)."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _rows(t, dtype, name, shape, dev):
     """Address and row stride of an [m, d] tensor whose rows are dense."""
     if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
@@ -147,11 +152,13 @@ def block_norm(residual, block=None, *, post_weight=None, gate=None, gate_act: s
     if residual_out is not None:
         op, os = _rows(residual_out, rt, "residual_out", shape, dev)
     elif block is not None:
-        residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+        residual_out = _like(residual)
         op, os = residual_out.data_ptr(), d
     if pre_weight is not None:
         if out is None:
-            out = torch.empty_like(residual, dtype=_BF16, memory_format=torch.contiguous_format)
+            like = residual if rt is _BF16 else block
+            out = _like(like) if like is not None else torch.empty_like(residual, dtype=_BF16,
+                                                                        memory_format=torch.contiguous_format)
             xp = out.data_ptr()
         else:
             xp = _dense(out, _BF16, "out", shape, dev)
@@ -257,7 +264,7 @@ def kv_append(q, k, v, inv_freq, kv: PagedKV, batch: PagedBatch, *, interleaved:
         qp, qs = _heads(q, "q", (T, None), kv)
         H = q.shape[1]
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _like(q)
             op = q_out.data_ptr()
         else:
             op = _dense(q_out, _BF16, "q_out", q.shape, kv._dev)
@@ -283,7 +290,7 @@ def attention(q, kv: PagedKV, batch: PagedBatch, *, scale: float | None = None, 
     qp, qs = _heads(q, "q", (None, None), kv)
     T, H, D = q.shape
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _like(q)
         op = out.data_ptr()
     else:
         op = _dense(out, _BF16, "out", q.shape, kv._dev)
