@@ -187,12 +187,6 @@ __device__ __forceinline__ void sum_block(int64_t &x, int64_t &y, Scan &sx, Scan
         x += sx.wave[i], y += sy.wave[i];
 }
 
-// a / b for a >= 0, b > 0: nearly always within 32 bits, where it is far cheaper.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
-{
-    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // Fills the group table.
 __device__ __forceinline__ void fill_groups(const Sched &s, Groups &gr)
 {
@@ -376,7 +370,8 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = __shfl(cell, i * RPI + lane / LPR);
-                vr[i] = *reinterpret_cast<const uint4 *>(a.v + (uint64_t)max(c, 0) * (D * ES) + lane % LPR * 16);
+                // whole lines, read once: past the caches (K, whose loads take half lines, through them)
+                vr[i] = ld_stream16(a.v + (uint64_t)max(c, 0) * (D * ES) + lane % LPR * 16);
                 v_held |= c >= 0 ? 1u << i : 0u;
             }
         };
