@@ -241,9 +241,10 @@ struct Listing {
 // piece of LDS; no barrier until the workgroup's run of one key head ends and
 // the four waves' states are joined.  Eight waves a CU with 16 KB each on the
 // way cover the memory latency (twelve with 8 KB of an 8-bit cache).  64 users
-// with up to 16000 keys each, 64 query heads over 8 of 128: 380 us, 5.6 TB/s;
-// one user's 200003 keys 152 us, 5.4 TB/s; 96 users on an 8-bit cache 95 us,
-// 4.7 TB/s; one user's 1531 keys 9 us: four memory latencies and a launch.
+// with up to 16000 keys each, 64 query heads over 8 of 128: 340 us, 6.2 TB/s
+// (V through the caches like K: 380); one user's 200003 keys 140 us, 5.9 TB/s
+// (152); 96 users on an 8-bit cache 78 us, 5.7 TB/s (95); one user's 1531 keys
+// 9 us: four memory latencies and a launch.
 // Workgroups of it that fit a CU, by their registers.
 constexpr int stream_per_cu(int d, bool e4m3, int nb) { return nb == 1 && (e4m3 || d == 64) ? 3 : 2; }
 
@@ -1250,12 +1251,16 @@ void start(const AttnArgs &a, const Plan &pl, hipStream_t st)
         attention_stream<D, E4M3, 1><<<grid, kThreads, 0, st>>>(a);
     else
         attention_stream<D, E4M3, 2><<<grid, kThreads, 0, st>>>(a);
-    // a workgroup for every four heads where tokens are few, else for sixteen
+    // a workgroup for every four heads where tokens are few, for sixteen, for a
+    // token (1052 tokens of 40 heads: 116 us with it, 120 by sixteen), for 16
+    // tokens where most are finished ones of prompts
     const unsigned T = (unsigned)s.p.b.n_tokens, heads = (unsigned)s.n_heads;
     if (T <= 64)
         attention_join<D, true><<<dim3(T, (heads + 3) / 4), kThreads, 0, st>>>(a, 1);
-    else if (T <= 2048)
+    else if (T <= 512)
         attention_join<D, false><<<dim3(T, (heads + 15) / 16), kThreads, 0, st>>>(a, 1);
+    else if (T <= 2048)
+        attention_join<D, false><<<dim3(T), kThreads, 0, st>>>(a, 1);
     else
         attention_join<D, false><<<dim3((T + 15) / 16), kThreads, 0, st>>>(a, 16);
 }

@@ -34,6 +34,9 @@ constexpr int kRunCost = 4;          // units that a run's beginning and end cos
 constexpr int kMinUnits = 4;         // units that are worth a workgroup: one a wave
 constexpr int kMinTiles = 4;         // key tiles that are worth a split
 constexpr int kItemCost = 5;         // key tiles that a tiled item's beginning and end cost
+constexpr float kSplitCost = 0.06f;  // key tiles that the states of one split of an item cost to write and join
+                                     // (0: 70 us for 128 users behind three prefixes, 52 for a chunk of 256 tokens
+                                     // beside 15 decodes; 0.06: 65 and 41)
 constexpr int kSharedNew = 16;       // new tokens a sequence up to which a group is shared
 constexpr int kTiledSlots = 512;     // workgroups of the tiled kernel that run at once
 
@@ -147,7 +150,8 @@ BD_HD int64_t tiled_work(const Sched &s, const Segment &g)
 // `work` key tiles in all were cut into k.
 BD_HD float tiled_time(int64_t items, int64_t work, int k)
 {
-    return ceilf((float)items * k / kTiledSlots) * (ceilf((float)work / ((float)items * k)) + kItemCost);
+    const float join = k > 1 ? kSplitCost * items * k : 0.0f;
+    return ceilf((float)items * k / kTiledSlots) * (ceilf((float)work / ((float)items * k)) + kItemCost) + join;
 }
 // Key tiles of a split where items are cut into k on the average.
 BD_HD int64_t tiled_depth(int64_t items, int64_t work, int k)
