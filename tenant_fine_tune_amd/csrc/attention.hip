@@ -554,10 +554,10 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
 // at 2.0 GHz and so is the vector unit: leaving out all exponentials saves 5%,
 // three quarters of the second product 10%, any one kind of LDS read 2-4%, so
 // what bounds a step is a wave's own chain of about 300 instructions at 8
-// cycles each, two waves a SIMD (a third has no registers).  Measured and
-// dropped: eight waves that share a tile, also half a step apart (430 us), 64
-// rows a wave at 128 columns, one wave a SIMD (640 us), K fragments read ahead
-// over the barrier (435 us).
+// cycles each, two waves a SIMD.  Measured and dropped: eight waves that share
+// a tile, also half a step apart (430 us), 64 rows a wave at 128 columns, one
+// wave a SIMD (640 us), K fragments read ahead over the barrier (435 us), steps
+// of 32 keys (465 us), with them a third wave a SIMD (510 us, registers spilled).
 template <int D>
 struct TiledLds {
     __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * Stride<D>::k], vt[2][kTileKeys * Stride<D>::v];

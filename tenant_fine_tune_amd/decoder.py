@@ -132,11 +132,12 @@ def block_norm(residual, block=None, *, post_weight=None, gate=None, gate_act: s
     weight = post_weight if pre_weight is None else pre_weight
     wt, n_variants, post, pre = 0, 1, 0, 0
     if weight is not None:
-        dtype, want = weight.dtype, weight.shape
+        dtype = weight.dtype if isinstance(weight, _Tensor) else None
         if dtype is not _BF16 and dtype is not _F32:
-            raise TypeError("weights must be bfloat16 or float32")
+            raise TypeError("weights must be bfloat16 or float32 tensors")
+        want = weight.shape
         wt = BD_F32 if dtype is _F32 else BD_BF16
-        if want[-1] != d or not 1 <= len(want) <= 2 or want[0] < 1:
+        if not 1 <= len(want) <= 2 or want[-1] != d or want[0] < 1:
             raise ValueError(f"weights must be [V, {d}] or [{d}] (got {list(want)})")
         n_variants = want[0] if len(want) == 2 else 1
         if post_weight is not None:

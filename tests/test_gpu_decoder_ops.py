@@ -111,6 +111,20 @@ def test_block_norm_in_place_zero_rows_and_empty(bd):
     assert r.shape == (0, 2056) and x.shape == (0, 2056)
 
 
+def test_block_norm_refuses_weights(bd):
+    res, blk, _, post, pre, ids = norm_inputs(2, 64, 3, "bf16", "bf16", False, 0, seed=4)
+    for w, error in ((1.0, TypeError), (pre.half(), TypeError), (pre[0, 0], ValueError), (pre[:0], ValueError),
+                     (pre[:, :-1], ValueError), (pre[None], ValueError)):
+        with pytest.raises(error, match="weights must be"):
+            bd.block_norm(res, blk, pre_weight=w, variant_ids=ids)
+    with pytest.raises(ValueError, match="pre_weight"):
+        bd.block_norm(res, blk, pre_weight=pre.t().contiguous().t(), variant_ids=ids)
+    with pytest.raises(ValueError, match="post_weight must be"):
+        bd.block_norm(res, blk, post_weight=post[:2], pre_weight=pre, variant_ids=ids)
+    with pytest.raises(ValueError, match="variant_ids"):
+        bd.block_norm(res, blk, pre_weight=pre)
+
+
 def test_block_norm_rows_do_not_mix(bd):
     """A NaN or an infinity stays in its own row."""
     res, blk, _, post, pre, _ = norm_inputs(8, 4104, 1, "bf16", "bf16", False, 0, seed=3)
