@@ -187,6 +187,14 @@ __device__ __forceinline__ void sum_block(int64_t &x, int64_t &y, Scan &sx, Scan
         x += sx.wave[i], y += sy.wave[i];
 }
 
+// a / b for a >= 0, b > 0: nearly always within 32 bits, where it is far cheaper
+// (in the schedule's sums, once a thread, it costs more registers than it saves time:
+// chunk of 1021 tokens beside 31 decodes 115 us with it there, 111 without).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Fills the group table.
 __device__ __forceinline__ void fill_groups(const Sched &s, Groups &gr)
 {

@@ -58,13 +58,7 @@ struct Segment {
     bool shared;                     // the group's prefix is taken once for all
 };
 
-// a / b for a >= 0, b > 0: nearly always within 32 bits, where the device does
-// it in 40 instructions instead of several hundred.
-BD_HD int64_t quotient(int64_t a, int64_t b)
-{
-    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-BD_HD int64_t cdiv(int64_t a, int64_t b) { return quotient(a + b - 1, b); }
+BD_HD int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Group g's entry of `gr` (and with the last group the end of the list).
 BD_HD void fill_group(const Sched &s, Groups &gr, int g)
@@ -161,7 +155,7 @@ BD_HD int64_t tiled_depth(int64_t items, int64_t work, int k)
 }
 BD_HD int tiled_splits(const Sched &s, const Segment &g, int64_t depth)
 {
-    const int64_t n = quotient(key_tiles(g, kTileKeys) + depth / 2, depth);
+    const int64_t n = (key_tiles(g, kTileKeys) + depth / 2) / depth;
     return (int)(n < 1 ? 1 : n > s.splits ? s.splits : n);
 }
 BD_HD int64_t tiled_items(const Sched &s, const Segment &g, int64_t depth)
