@@ -9,7 +9,7 @@
 // loads of a row are issued before the first sum is waited for; the second
 // sum needs only what is in registers.  Sums and norms are fp32, r' enters the
 // second norm before its rounding.  4096 x 8192 bf16 takes 55 us (4.9 TB/s),
-// 4099 x 8192 with an fp32 residual and a gate 96 us (4.9 TB/s; a copy of 2 GiB
+// 4099 x 8192 with an fp32 residual and a gate 93 us (5.0 TB/s; a copy of 2 GiB
 // reaches 5.4), four rows 5 us, of which the launch is most.
 #include "bd_device.h"
 #include "decoder_launch.h"
