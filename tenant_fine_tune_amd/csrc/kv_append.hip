@@ -5,12 +5,15 @@
 // angle pos * inv_freq[i] is formed and reduced to a fraction of a turn in
 // fp64, because a position of 10^6 leaves fp32 no digits of a fast angle; the
 // sine and cosine of the fraction are fp32, computed once per token and pair
-// into LDS and shared by all heads.  A thread then moves two 8-column chunks
-// of a head: the two halves of eight pairs, or 16 neighbouring columns.
-// Memory bound: every q, k, v is read once and written once (7531 tokens of 64 +
-// 8 + 8 heads of 128 into an 8-bit cache: 38 us with its inputs in the last
-// cache level, 49 us from HBM, 4.8 TB/s; 32 single tokens 5 us, launch latency:
-// their heads are dealt over three workgroups each).
+// into LDS and shared by all heads.  A thread then moves two 8-column chunks of
+// a head, half of the turned (or of the other) columns apart: eight pairs of
+// halves, or eight neighbouring pairs, and neighbouring threads touch whole
+// lines.  Memory bound: every q, k, v is read once, past the caches, and written
+// once, q past them too where its lines are whole: 17122 tokens of 64 + 8 + 8
+// heads of 128 take 120 us, 6.0 TB/s (133 through the caches); half-turned heads
+// 51 us (54 with their half lines past the caches).  7531 tokens into an 8-bit
+// cache, half turned: 48 us from HBM, 4.9 TB/s; 32 single tokens 5 us, launch
+// latency: their heads are dealt over three workgroups each.
 #include "bd_device.h"
 #include "decoder_launch.h"
 #include "paged.h"
@@ -101,20 +104,20 @@ __global__ __launch_bounds__(kThreads) void append_tokens(AppendArgs a)
             continue;
         const int head = is_q ? row : is_v ? row - H - p.n_kv : row - H;
         const bool turned = !is_v && part * 16 < a.rotary;
-        // columns of the two chunks: the halves of eight pairs, or neighbours
-        const int c0 = turned && !INTER ? part * 8 : part * 16;
-        const int c1 = turned && !INTER ? a.rotary / 2 + part * 8 : c0 + 8;
+        // the two chunks: the same place in the halves of what is turned, or of what is not
+        const int from = turned || is_v ? 0 : a.rotary, width = turned ? a.rotary : D - from;
+        const int c0 = from + (part - from / 16) * 8, c1 = c0 + width / 2;
         float x[8], y[8];
         if (placed) {
             const uint16_t *src = (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) +
                                   (int64_t)head * D;
-            unpack8(*reinterpret_cast<const uint4 *>(src + c0), x);
-            unpack8(*reinterpret_cast<const uint4 *>(src + c1), y);
+            unpack8(ld_stream16(src + c0), x);
+            unpack8(ld_stream16(src + c1), y);
             if (turned) {
                 if (INTER) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 e = turn[part * 8 + i], f = turn[part * 8 + 4 + i];
+                        const float2 e = turn[c0 / 2 + i], f = turn[c1 / 2 + i];
                         const float x0 = x[2 * i], y0 = y[2 * i];
                         x[2 * i] = x0 * e.x - x[2 * i + 1] * e.y;
                         x[2 * i + 1] = x[2 * i + 1] * e.x + x0 * e.y;
@@ -138,8 +141,13 @@ __global__ __launch_bounds__(kThreads) void append_tokens(AppendArgs a)
         }
         if (is_q) {
             uint16_t *dst = a.q_out + (t * H + head) * D;
-            *reinterpret_cast<uint4 *>(dst + c0) = pack8(x);
-            *reinterpret_cast<uint4 *>(dst + c1) = pack8(y);
+            if (width == D) {
+                st_stream16(dst + c0, pack8(x));
+                st_stream16(dst + c1, pack8(y));
+            } else {
+                *reinterpret_cast<uint4 *>(dst + c0) = pack8(x);
+                *reinterpret_cast<uint4 *>(dst + c1) = pack8(y);
+            }
         } else {
             const int64_t at = cell + ((int64_t)head << p.page_shift);
             const float *scales = is_v ? a.v_scale : a.k_scale;
