@@ -11,9 +11,12 @@
 // lines.  Memory bound: every q, k, v is read once, past the caches, and written
 // once, q past them too where its lines are whole: 17122 tokens of 64 + 8 + 8
 // heads of 128 take 120 us, 6.0 TB/s (133 through the caches); half-turned heads
-// 51 us (54 with their half lines past the caches).  7531 tokens into an 8-bit
-// cache, half turned: 48 us from HBM, 4.9 TB/s; 32 single tokens 5 us, launch
-// latency: their heads are dealt over three workgroups each.
+// 51 us (54 with their half lines past the caches).  Between the kernels that
+// write its inputs and read q, 17122 tokens gain the same (368 -> 344 us for all
+// three), 6060 more (153 -> 129), 2015, which the last cache level holds, lose
+// (47 -> 50).  7531 tokens into an 8-bit cache, half turned: 48 us from HBM, 4.9
+// TB/s; 32 single tokens 5 us, launch latency: their heads are dealt over three
+// workgroups each.
 #include "bd_device.h"
 #include "decoder_launch.h"
 #include "paged.h"
