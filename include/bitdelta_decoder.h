@@ -36,7 +36,7 @@ extern "C" {
  * gate: bf16 [m, d]; each with its own row stride in elements (>= d); x: bf16
  * [m, d], dense.  post_weight, pre_weight: [n_variants, d] of weight_dtype, dense.
  * A token whose id is outside [0, n_variants) gets a zero row of x and
- * r' = residual.
+ * r' = residual.  With neither weight the ids pick nothing and are not read.
  * Element alignment is enough; rows that start on 16 bytes load fastest.
  * 1 <= d <= BD_NORM_MAX_WIDTH (BD_ESHAPE otherwise). */
 #define BD_NORM_MAX_WIDTH 32768

@@ -19,8 +19,8 @@ class AttentionBlock:
     """qkv and out: (w_base bf16 [d_out, d_in], signs uint8 [V, d_out, d_in/8],
     alpha fp32 [V, d_out]) of the two projections; the rows of qkv are those of
     q, k and v after one another, head by head.  post_weight (norm of the
-    block's output, or None) and next_weight (norm before the next block):
-    [V, d].  inv_freq: fp64 [rotary / 2] on the device."""
+    block's output) and next_weight (norm before the next block): [V, d], both
+    [d] for every variant, or None.  inv_freq: fp64 [rotary / 2] on the device."""
 
     def __init__(self, qkv, out, n_heads, kv, inv_freq, *, post_weight=None, next_weight=None, scale=1.0, eps=1e-6,
                  interleaved=False):

@@ -638,7 +638,9 @@ bd_status bitdelta_block_norm(const void *residual, int64_t residual_stride, int
     BD_ALIGNED(variant_ids, 4);
     bd::NormArgs a;
     a.residual = residual, a.block = block, a.gate = gate, a.post_weight = post_weight, a.pre_weight = pre_weight;
-    a.ids = variant_ids, a.residual_out = residual_out, a.x = x;
+    // without weights there is nothing for an id to be outside of
+    a.ids = post_weight || pre_weight ? variant_ids : nullptr;
+    a.residual_out = residual_out, a.x = x;
     a.residual_stride = residual_stride, a.block_stride = block_stride, a.gate_stride = gate_stride;
     a.out_stride = residual_out_stride, a.m = m;
     a.n_variants = n_variants, a.d = (int32_t)d, a.gate_act = gate_act, a.scale = scale, a.eps = eps;

@@ -106,8 +106,9 @@ def block_norm(residual, block=None, *, post_weight=None, gate=None, gate_act: s
     x = rms(r') * pre_weight[v], v = variant_ids[token].
 
     residual bf16 or fp32 [m, d]; block, gate bf16 [m, d]; weights bf16 or
-    fp32 (both the same) [V, d] or [d]; variant_ids int32 [m] (needed where
-    V > 1).  Rows may be strided.  block None: no update; post_weight None: the
+    fp32 (both the same) [V, d], or [d] for every variant; variant_ids int32
+    [m] (needed where V > 1; they pick nothing where the weights are [d] or
+    None).  Rows may be strided.  block None: no update; post_weight None: the
     block is added as it is; pre_weight None: no x.  residual_out may be
     residual (in place); None allocates it where there is a block.  Returns
     (r', x): r' is `residual` without a block, x None without pre_weight."""
@@ -147,6 +148,8 @@ def block_norm(residual, block=None, *, post_weight=None, gate=None, gate_act: s
     ids = 0
     if variant_ids is not None:
         ids = _dense(variant_ids, _I32, "variant_ids", (m,), dev)
+        if weight is None or weight.dim() == 1:
+            ids = 0        # nothing to pick: no weight, or one for every variant
     elif n_variants > 1:
         raise ValueError("weights of several variants need variant_ids")
     op = os = xp = 0
