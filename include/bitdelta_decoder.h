@@ -79,7 +79,8 @@ typedef struct {
  * prefix_len[g] keys in the pages prefix_table[g, :] (int32 [n_groups,
  * max_prefix_pages]): every token of the group sees all of them, and its
  * position is prefix_len[g] + its place.  n_groups = 0: no prefixes, the
- * three pointers may be NULL.
+ * three pointers may be NULL.  n_seqs = 0: padding alone, the three pointers
+ * of the sequences may be NULL, with groups or without.
  * Bounds kept on the device: starts are clamped to [0, n_tokens], lengths to
  * what the table's columns hold and to 2^30; a place below 0 or a page number outside
  * [0, n_pages) holds no key (nothing is stored there and attention passes it

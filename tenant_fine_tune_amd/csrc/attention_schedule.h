@@ -68,8 +68,9 @@ BD_HD void fill_group(const Sched &s, Groups &gr, int g)
     if (g == s.p.b.n_groups - 1)
         gr.begin[g + 1] = b;
     gr.prefix[g] = prefix_keys(s.p, g);
-    const int64_t toks = (int64_t)seq_begin(s.p, b) - seq_begin(s.p, a);
-    gr.shared[g] = s.tiled && b - a >= 2 && gr.prefix[g] > 0 && toks > 0 && toks <= (int64_t)kSharedNew * (b - a);
+    // a batch without sequences has no starts to read
+    const int64_t toks = b - a >= 2 ? (int64_t)seq_begin(s.p, b) - seq_begin(s.p, a) : 0;
+    gr.shared[g] = s.tiled && gr.prefix[g] > 0 && toks > 0 && toks <= (int64_t)kSharedNew * (b - a);
 }
 
 BD_HD Segment sequence(const Sched &s, const Groups &gr, int i)
