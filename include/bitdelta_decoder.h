@@ -56,7 +56,9 @@ BD_API bd_status bitdelta_block_norm(const void *residual, int64_t residual_stri
  * page_size: a power of two in [1, 1024]; head_dim: 64 or 128; n_kv_heads at
  * most 1024; n_pages * n_kv_heads * page_size below 2^31.
  * dtype BD_KV_E4M3: a stored number stands for number * scale[head], with
- * k_scale / v_scale fp32 [n_kv_heads] (NULL: 1); BD_KV_BF16 takes no scales. */
+ * k_scale / v_scale fp32 [n_kv_heads] (NULL: 1), of any sign or zero (an
+ * append divides by them: by zero it stores +-448, and NaN for a zero);
+ * BD_KV_BF16 takes no scales. */
 typedef enum { BD_KV_BF16 = 0, BD_KV_E4M3 = 1 } bd_kv_dtype;
 
 typedef struct {

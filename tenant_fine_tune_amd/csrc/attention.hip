@@ -118,6 +118,24 @@ __device__ __forceinline__ float max_of_halves(float x)
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// Scores are masked and compared before they are scaled, which needs a factor
+// above zero.  What else an 8-bit cache's scale gives goes into the row's q: the
+// sign, or a zero, which leaves there what is not finite as a NaN.
+template <typename Q>
+__device__ __forceinline__ float positive_factor(float sc, Q &q)
+{
+    if (sc <= 0.0f) {
+        const float f = sc < 0.0f ? -1.0f : 0.0f;
+        for (auto &block : q)
+            for (auto &k : block)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    k[i] = (__bf16)((float)k[i] * f);
+        sc = sc < 0.0f ? -sc : 1.0f;
+    }
+    return sc;
+}
+
 // Waits for this wave's LDS accesses.
 __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
@@ -356,7 +374,7 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
             for (int d = 0; d < DB; ++d)
                 o[n][d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
         }
-        const float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
+        float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
 
         // lane l: the cell of the tile's key l % 32
         const auto cells = [&](int t) {
@@ -391,6 +409,8 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
         }
         if (t + kWaves < t1)
             next = cells(t + kWaves);
+        if (E4M3)
+            sc = positive_factor(sc, q);
         for (; t < t1; t += kWaves) {
             const uint32_t held = (uint32_t)__ballot(cell >= 0);
             const bool own = t >= pre_tiles;
@@ -693,7 +713,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                 for (int r = 0; r < 16; ++r)
                     o[n][d][r] = 0.0f;
         }
-        const float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
+        float sc = a.scale * kLog2e * (E4M3 && a.k_scale ? a.k_scale[head] : 1.0f);
 
         // One set of registers carries K of the next tile until the scores of
         // this one are done, then its V.  A key without a cell reads cell 0: its
@@ -781,6 +801,8 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
         };
         // q has to be there before the loop: its wait inside would be one for all loads in flight
         wait_vmcnt<0>();
+        if (E4M3)
+            sc = positive_factor(sc, q);
         if (t0 < t1) {
             // past the end the last tile is read once more, and dropped
             read_page(t0);
