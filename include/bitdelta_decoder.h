@@ -126,8 +126,10 @@ BD_API bd_status bitdelta_kv_append(const bd_bf16 *q, int64_t q_stride, const bd
  * the keys j that token t sees (the prefix of its group, then its own places
  * up to its own), G = n_heads / n_kv_heads whole.  fp32 scores and sums, the
  * weights enter the second product in bf16, the output is rounded once.
- * A token that sees no key, and a padding token, gives a zero row.  Cells that
- * no token sees may hold anything, NaN included.
+ * A token that sees no key, and a padding token, gives a zero row, and so does
+ * one all of whose scores are -inf.  Cells that no token sees may hold anything,
+ * NaN included; what is not finite in a key or value goes into the sums of the
+ * tokens that see it, as the formula has it, and into no others.
  * q: bf16 [n_tokens, n_heads, head_dim], token stride in elements (a multiple
  * of 8), heads dense; out: the same, dense; q and out 16-byte aligned.
  * workspace: at least bitdelta_attention_workspace() bytes, 16-byte aligned,

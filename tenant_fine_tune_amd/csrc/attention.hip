@@ -143,20 +143,36 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 
 // Where a column of V holds a number that is not finite, a weight of zero does
 // not keep it out of the rows that do not see its key.  In tiles that some of
-// the rows see only in part such numbers are therefore taken out of V, and the
-// rows that do see them are set to NaN afterwards.  This clears them in eight
-// bf16 numbers and returns which they were.
+// the rows see only in part such numbers are therefore taken out of V and added
+// afterwards to the rows that do see them.  This takes them out of eight bf16
+// numbers and returns where they were; what they were stays in their place: an
+// infinity a zero of its sign, a NaN the least number (e4m3 has only NaN).
+template <bool E4M3>
 __device__ __forceinline__ uint32_t take_nonfinite(uint4 &w)
 {
     uint32_t bits = 0;
-    const auto one = [&](uint32_t &x, int i) {
-        if ((x & 0x7F80u) == 0x7F80u)
-            x &= 0xFFFF0000u, bits |= 1u << (2 * i);
-        if ((x & 0x7F800000u) == 0x7F800000u)
-            x &= 0xFFFFu, bits |= 2u << (2 * i);
+    const auto look = [&](uint32_t x, int i) {
+        bits |= (x & 0x7F80u) == 0x7F80u ? 1u << (2 * i) : 0u;
+        bits |= (x & 0x7F800000u) == 0x7F800000u ? 2u << (2 * i) : 0u;
     };
-    one(w.x, 0), one(w.y, 1), one(w.z, 2), one(w.w, 3);
+    look(w.x, 0), look(w.y, 1), look(w.z, 2), look(w.w, 3);
+    if (__builtin_expect(__any(bits != 0), 0)) {
+        const auto take = [&](uint32_t &x) {
+            if ((x & 0x7F80u) == 0x7F80u)
+                x = E4M3 ? x & 0xFFFF0000u : (x & 0xFFFF8000u) | ((x & 0x7Fu) != 0);
+            if ((x & 0x7F800000u) == 0x7F800000u)
+                x = E4M3 ? x & 0xFFFFu : (x & 0x8000FFFFu) | ((x & 0x7F0000u) != 0) << 16;
+        };
+        take(w.x), take(w.y), take(w.z), take(w.w);
+    }
     return bits;
+}
+
+// x with the number added that take_nonfinite left as p.
+template <bool E4M3>
+__device__ __forceinline__ float add_taken(float x, uint32_t p)
+{
+    return E4M3 || (p & 0x7FFFu) ? NAN : x + (p ? -INFINITY : INFINITY);
 }
 
 // The lowest n bits (none for n < 0, all from 64 on).
@@ -429,7 +445,7 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
                     if (masked) {
                         if (!((v_held >> i) & 1u))
                             w[e] = make_uint4(0, 0, 0, 0);
-                        const uint32_t bits = take_nonfinite(w[e]);
+                        const uint32_t bits = take_nonfinite<E4M3>(w[e]);
                         bad[wave][r][c + e] = (uint8_t)bits;
                         any_bad |= bits;
                     }
@@ -501,18 +517,21 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
                 for (int n = 0; n < NB; ++n)
                     o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[n], o[n][d], 0, 0, 0);
             }
-            if (masked && __any(any_bad != 0)) {
+            if (masked && __builtin_expect(__any(any_bad != 0), 0)) {
 #pragma unroll 1
                 for (int key = 0; key < kStreamKeys; ++key)
 #pragma unroll
                     for (int d = 0; d < DB; ++d) {
-                        const int bits = bad[wave][key][2 * d + (quad >> 1)] >> (quad & 1) * 4;
+                        const int bits = bad[wave][key][2 * d + (quad >> 1)] >> (quad & 1) * 4 & 15;
+                        if (!bits)
+                            continue;
+                        const u32x2 was = *reinterpret_cast<const u32x2 *>(vt + key * VS + d * 16 + quad * 4);
 #pragma unroll
                         for (int n = 0; n < NB; ++n)
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 if (((bits >> r) & 1) && (!own || key < seen[n] - j0))
-                                    o[n][d][r] = NAN;
+                                    o[n][d][r] = add_taken<E4M3>(o[n][d][r], was[r >> 1] >> 16 * (r & 1) & 0xFFFFu);
                     }
             }
         }
@@ -789,7 +808,7 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
                     if (cell < 0)
                         v[e] = make_uint4(0, 0, 0, 0);
                     if (partial(t)) {
-                        const uint32_t bits = take_nonfinite(v[e]);
+                        const uint32_t bits = take_nonfinite<E4M3>(v[e]);
                         bad[buf][ldr][ldc + i * STEP + e] = (uint8_t)bits;
                         found_bad |= bits;
                     }
@@ -972,18 +991,22 @@ __device__ __forceinline__ void tiled_body(const AttnArgs &a, TiledLds<D> &sh, i
 #pragma unroll
                     for (int w = 0; w < kWaves; ++w)
                         some |= any_bad[buf][w] == now;
-                if (some) {
+                if (__builtin_expect(some, 0)) {
 #pragma unroll 1
                     for (int key = 0; key < kTileKeys; ++key)
 #pragma unroll
                         for (int c = 0; c < D / 8; ++c) {
-                            const int bits = any_bad[buf][key >> 4] == now ? bad[buf][key][c] >> half * 4 : 0;
+                            const int bits = any_bad[buf][key >> 4] == now ? bad[buf][key][c] >> half * 4 & 15 : 0;
+                            if (!bits)
+                                continue;
+                            const u32x2 was = *reinterpret_cast<const u32x2 *>(vt[buf] + key * VR + c * 8 + half * 4);
 #pragma unroll
                             for (int n = 0; n < NR; ++n)
 #pragma unroll
                                 for (int r = 0; r < 4; ++r)
                                     if (((bits >> r) & 1) && key < seen[n] - j0)
-                                        o[n][c >> 2][(c & 3) * 4 + r] = NAN;
+                                        o[n][c >> 2][(c & 3) * 4 + r] = add_taken<E4M3>(
+                                            o[n][c >> 2][(c & 3) * 4 + r], was[r >> 1] >> 16 * (r & 1) & 0xFFFFu);
                         }
                 }
             }
