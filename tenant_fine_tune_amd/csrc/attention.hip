@@ -1255,6 +1255,9 @@ __global__ __launch_bounds__(kThreads) void attention_join(AttnArgs a, int token
 
 // ------------------------------------------------------------------------ host
 
+// Workgroups of a launch, so that their threads stay below 2^32; more items go round.
+constexpr int64_t kMaxItems = 1 << 23;
+
 struct Plan {
     Sched s;
     int64_t grid, rows;     // workgroups, rows of partial states
@@ -1285,7 +1288,7 @@ Plan make_plan(int32_t n_heads, const bd_kv_cache &c, const bd_batch &b)
     // a workgroup per item; where items are split they are few, and the bound is loose
     const int64_t full = T * s.group / s.tile_rows;
     const int64_t row_tiles = full + (b.n_seqs < T ? b.n_seqs : T) + (b.n_groups > 0 ? full + b.n_groups : 0);
-    const int64_t items = row_tiles * c.n_kv_heads * s.splits, cap = s.splits > 1 ? 2 * kTiledSlots : INT_MAX;
+    const int64_t items = row_tiles * c.n_kv_heads * s.splits, cap = s.splits > 1 ? 2 * kTiledSlots : kMaxItems;
     const int64_t tiled_wgs = items < s.stream_wgs ? s.stream_wgs : items < cap ? items : cap;
     pl.grid = s.stream_wgs + (s.tiled ? tiled_wgs : 0);
     return pl;
@@ -1314,8 +1317,10 @@ void start(const AttnArgs &a, const Plan &pl, hipStream_t st)
         attention_join<D, false><<<dim3(T, (heads + 15) / 16), kThreads, 0, st>>>(a, 1);
     else if (T <= 2048)
         attention_join<D, false><<<dim3(T), kThreads, 0, st>>>(a, 1);
-    else
-        attention_join<D, false><<<dim3((T + 15) / 16), kThreads, 0, st>>>(a, 16);
+    else {
+        const unsigned each = T <= 16 * kTokensAcross ? 16 : (unsigned)cdiv(T, kTokensAcross);
+        attention_join<D, false><<<dim3((unsigned)cdiv(T, each)), kThreads, 0, st>>>(a, (int)each);
+    }
 }
 
 }  // namespace

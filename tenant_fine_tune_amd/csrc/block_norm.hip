@@ -132,7 +132,9 @@ template <int C, typename RT, typename WT>
 __global__ __launch_bounds__(1024, C == 1 ? 8 : 4) void block_norm_rows(NormArgs a)
 {
     __shared__ float part[2][16];
-    const int64_t i = blockIdx.x;
+    const int64_t i = blockIdx.y * kTokensAcross + blockIdx.x;
+    if (i >= a.m)
+        return;
     const int d = a.d, T = blockDim.x;
     const int v = a.ids ? a.ids[i] : 0;
     const bool known = (unsigned)v < (unsigned)a.n_variants;
@@ -221,7 +223,8 @@ void start(const NormArgs &a, hipStream_t s)
 {
     // as many waves as the row has groups of 512 columns
     const int threads = (a.d + 512 * C - 1) / (512 * C) * 64;
-    const dim3 grid((unsigned)a.m);
+    const dim3 grid((unsigned)(a.m < kTokensAcross ? a.m : kTokensAcross),
+                    (unsigned)((a.m + kTokensAcross - 1) / kTokensAcross));
     if (a.residual_f32) {
         if (a.weight_f32)
             block_norm_rows<C, float, float><<<grid, threads, 0, s>>>(a);

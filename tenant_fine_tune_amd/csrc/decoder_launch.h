@@ -10,6 +10,10 @@
 
 namespace bd {
 
+// Workgroups of one dimension of a launch by token: a dimension of 2^32 threads
+// or more wraps around without an error, so tokens past these go into another.
+constexpr int64_t kTokensAcross = 1 << 20;
+
 struct NormArgs {
     const void *residual;
     const uint16_t *block, *gate;

@@ -76,7 +76,9 @@ __global__ __launch_bounds__(kThreads) void append_tokens(AppendArgs a)
 {
     __shared__ float2 turn[D / 2];
     const Paged &p = a.p;
-    const int64_t t = blockIdx.x;
+    const int64_t t = blockIdx.z * kTokensAcross + blockIdx.x;
+    if (t >= p.b.n_tokens)
+        return;
     const int s = seq_of(p, t);
     bool placed = s >= 0;
     int64_t cell = -1;   // of head 0
@@ -195,7 +197,8 @@ hipError_t launch_kv_append(const uint16_t *q, int64_t q_stride, const uint16_t 
     a.n_heads = n_heads, a.rotary = rotary;
     const int64_t units = (int64_t)(n_heads + 2 * c.n_kv_heads) * (c.head_dim / 16);
     const int64_t parts = b.n_tokens < 512 ? (units + kThreads - 1) / kThreads : 1;
-    const dim3 grid((unsigned)b.n_tokens, (unsigned)parts);
+    const dim3 grid((unsigned)(b.n_tokens < kTokensAcross ? b.n_tokens : kTokensAcross), (unsigned)parts,
+                    (unsigned)((b.n_tokens + kTokensAcross - 1) / kTokensAcross));
     if (c.head_dim == 64)
         start<64>(a, c.dtype == BD_KV_E4M3, interleaved, grid, s);
     else
