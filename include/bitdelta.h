@@ -35,7 +35,10 @@
  *    16-byte aligned, alpha and variant ids 4-byte aligned, workspaces as
  *    stated per call; signs need no alignment (bitdelta_similarity: 4).
  *  - d_in must be a positive multiple of 8 (whole sign bytes); d_out > 0;
- *    m >= 0 (m = 0 is a no-op returning BD_OK).
+ *    m >= 0 (m = 0 is a no-op returning BD_OK).  A launch takes fewer than
+ *    2^32 threads: compress and reconstruct (256 a row, reconstruct per 2048
+ *    columns), similarity_delta (64 to 640) and the decode of rows narrower
+ *    than 16 (64) refuse more rows than that with BD_ESHAPE.
  *  - Calls are thread-safe; concurrent calls on different streams may share
  *    read-only inputs.
  */

@@ -39,6 +39,9 @@ bd_status device(hipError_t e, const char *what)
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxGrid = std::numeric_limits<int32_t>::max();
+// Workgroups of `threads` of one launch: from 2^32 threads on it wraps around
+// without an error.
+constexpr int64_t max_workgroups(int64_t threads) { return std::numeric_limits<uint32_t>::max() / threads; }
 
 bd_status check_matrix(int64_t d_out, int64_t d_in)
 {
@@ -124,6 +127,8 @@ bd_status bitdelta_compress(const bd_bf16 *w_base, const void *w_ft, int ft_dtyp
     if (ft_dtype != BD_BF16 && ft_dtype != BD_F32)
         return fail(BD_EINVAL, "ft_dtype must be BD_BF16 (0) or BD_F32 (1), got %d", ft_dtype);
     BD_TRY(check_matrix(d_out, d_in));
+    if (d_out > max_workgroups(256))
+        return fail(BD_ESHAPE, "matrix [%lld, %lld] exceeds the compress grid", (long long)d_out, (long long)d_in);
     BD_NONNULL(w_base);
     BD_NONNULL(w_ft);
     BD_NONNULL(signs);
@@ -158,7 +163,7 @@ bd_status bitdelta_reconstruct(const bd_bf16 *w_base, const uint8_t *signs, cons
     BD_ALIGNED(w_eff, 16);
     BD_ALIGNED(alpha, 4);
     const int64_t bpr = (d_in / 8 + 255) / 256;
-    if (d_out * bpr > kMaxGrid)
+    if (bpr > max_workgroups(256) || d_out > max_workgroups(256) / bpr)
         return fail(BD_ESHAPE, "matrix [%lld, %lld] exceeds the reconstruct grid", (long long)d_out, (long long)d_in);
     return device(bd::launch_reconstruct(w_base, signs, alpha, alpha_mode == BD_ALPHA_MATRIX, d_out, d_in, w_eff,
                                          (hipStream_t)stream),
@@ -212,6 +217,10 @@ bd_status bitdelta_linear(const bd_bf16 *x, int64_t m, const bd_bf16 *w_base, co
         // least 16 rows) through 32-bit buffer offsets.
         if ((int64_t)bd::kGemvMaxM * d_in * 2 >= ((int64_t)1 << 31))
             return fail(BD_ESHAPE, "decode linear needs 16 rows of W_base below 2 GiB (d_in=%lld)", (long long)d_in);
+        // (chunks of wider rows are below 2 GiB / 32 rows, at most 64 threads each)
+        if (d_in < 16 && d_out > max_workgroups(64))
+            return fail(BD_ESHAPE, "linear d_out=%lld of width %lld exceeds the decode grid", (long long)d_out,
+                        (long long)d_in);
         return device(bd::launch_gemv(x, (int)m, w_base, signs, alpha, per_matrix, d_out, d_in, y, workspace, s),
                       "bitdelta_linear (decode)");
     }
@@ -384,6 +393,10 @@ bd_status bitdelta_similarity_delta(const bd_bf16 *w_base, const void *w_ft, int
     if (n_variants < 1 || n_variants > bd::kSimilarityMaxVariants)
         return fail(BD_EINVAL, "n_variants must be in [1, %d] (got %d)", bd::kSimilarityMaxVariants, n_variants);
     BD_TRY(check_matrix(d_out, d_in));
+    // a row's workgroup has a wave for each pair of tiles of four variants
+    const int tiles = (n_variants + 3) / 4;
+    if (d_out > max_workgroups(64 * tiles * (tiles + 1) / 2))
+        return fail(BD_ESHAPE, "matrix [%lld, %lld] exceeds the similarity_delta grid", (long long)d_out, (long long)d_in);
     const size_t need = bitdelta_similarity_delta_workspace(n_variants, d_out, d_in);
     if (workspace_bytes < need)
         return fail(BD_EWORKSPACE, "similarity_delta needs %zu workspace bytes, got %zu", need, workspace_bytes);
