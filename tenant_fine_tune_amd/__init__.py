@@ -94,6 +94,12 @@ class BitDeltaError(RuntimeError):
 def _load():
     if not os.path.exists(lib_path):
         raise ImportError(f"libbitdelta.so is not built at {lib_path}; run __graft_entry__.build()")
+    # torch first: the library then runs on torch's HIP runtime.  Loaded before
+    # it, it would bring the system's, and see no device beside torch's.
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass           # the delta cache needs none
     handle = ctypes.CDLL(lib_path)
     for name, (res, args) in EXPORTS.items():
         fn = getattr(handle, name)
@@ -477,7 +483,7 @@ _DECODER = ("block_norm", "kv_append", "attention", "PagedKV", "PagedBatch")
 
 def __getattr__(name):
     # the operators between the linears; their module needs torch, which the
-    # package itself imports only when a call does
+    # package itself does without where there is none
     if name in _DECODER:
         from . import decoder
 
