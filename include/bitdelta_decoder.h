@@ -88,8 +88,9 @@ typedef struct {
  * [0, n_pages) holds no key (nothing is stored there and attention passes it
  * over).
  * max_new: the largest number of new tokens of one sequence, or 0 where the
- * caller does not know it; a hint for the choice of kernels that no result
- * depends on.  n_seqs <= BD_MAX_SEQS, n_groups <= BD_MAX_GROUPS; n_tokens < 2^31, and
+ * caller does not know it; a hint for the choice of kernels, right or wrong: by
+ * it the keys are summed in another order, and results agree within their
+ * roundings.  n_seqs <= BD_MAX_SEQS, n_groups <= BD_MAX_GROUPS; n_tokens < 2^31, and
  * n_tokens * n_heads < 2^31 in the calls that take queries. */
 #define BD_MAX_SEQS 4096
 #define BD_MAX_GROUPS 256

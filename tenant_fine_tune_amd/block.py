@@ -5,8 +5,8 @@ cache; this module runs the layer around its linears the same way: one fused
 q/k/v projection and one output projection through bitdelta_linear_grouped,
 and between them the rotated append to the paged cache, attention over it, and
 the norms, whose weights a variant keeps for itself (BitDelta codes the
-linears only).  Every call is one launch for the whole batch, whatever
-variants and sequences it mixes.
+linears only).  Every call takes the whole batch at once, whatever variants
+and sequences it mixes.
 """
 from __future__ import annotations
 

@@ -285,7 +285,7 @@ struct Listing {
 // way cover the memory latency (twelve with 8 KB of an 8-bit cache).  64 users
 // with up to 16000 keys each, 64 query heads over 8 of 128: 340 us, 6.2 TB/s
 // (V through the caches like K: 380); one user's 200003 keys 140 us, 5.9 TB/s
-// (152); 96 users on an 8-bit cache 78 us, 5.7 TB/s (95); one user's 1531 keys
+// (152); 96 users on an 8-bit cache 74 us, 6.0 TB/s (95); one user's 1531 keys
 // 9 us: four memory latencies and a launch.
 // Workgroups of it that fit a CU, by their registers.
 constexpr int stream_per_cu(int d, bool e4m3, int nb) { return nb == 1 && (e4m3 || d == 64) ? 3 : 2; }
@@ -596,15 +596,19 @@ __device__ __forceinline__ void stream_body(const AttnArgs &a, StreamLds<D, NB> 
 // a wave (256 and 64 at 64 columns), and walks 64-key tiles of K and V that all
 // four waves read from LDS; a tile's loads are in registers one step ahead, and
 // LDS holds two tiles, so a step has one barrier.  Prompts of up to 4097 tokens,
-// 64 heads over 8 of 128: 420 us, 818 TFLOP/s of the causal work (a large bf16
-// product reaches 1398 here).  The matrix units are busy 35-40% of the cycles
-// at 2.0 GHz and so is the vector unit: leaving out all exponentials saves 5%,
-// three quarters of the second product 10%, any one kind of LDS read 2-4%, so
-// what bounds a step is a wave's own chain of about 300 instructions at 8
-// cycles each, two waves a SIMD.  Measured and dropped: eight waves that share
+// 64 heads over 8 of 128: 424 us, 811 TFLOP/s of the causal work (a large bf16
+// product reaches 1398 here).  A wave's step of 128 columns is 413 instructions,
+// 32 of them matrix instructions of 32 cycles, and takes 5060 cycles beside the
+// SIMD's other wave (4500 alone): 37% issuing, 38% ready but behind the other
+// wave or the matrix unit, 25% waiting for loads, LDS or the barrier, with one
+// tile on its way in one set of registers.  The matrix units are busy 40% of the
+// cycles; leaving out all exponentials saves 5%, three quarters of the second
+// product 10%, any one kind of LDS read 2-4%.  Measured and dropped: eight waves that share
 // a tile, also half a step apart (430 us), 64 rows a wave at 128 columns, one
 // wave a SIMD (640 us), K fragments read ahead over the barrier (435 us), steps
 // of 32 keys (465 us), with them a third wave a SIMD (510 us, registers spilled).
+// As built the kernels at 256 registers spill 4 of them at 128 columns in bf16, 2
+// to 6 at 64 columns, and 45 to 70 scalars, once an item; no step touches scratch.
 template <int D>
 struct TiledLds {
     __attribute__((aligned(16))) uint16_t kt[2][kTileKeys * Stride<D>::k], vt[2][kTileKeys * Stride<D>::v];

@@ -35,8 +35,8 @@ constexpr int kMinUnits = 4;         // units that are worth a workgroup: one a 
 constexpr int kMinTiles = 4;         // key tiles that are worth a split
 constexpr int kItemCost = 5;         // key tiles that a tiled item's beginning and end cost
 constexpr float kSplitCost = 0.06f;  // key tiles that the states of one split of an item cost to write and join
-                                     // (0: 70 us for 128 users behind three prefixes, 52 for a chunk of 256 tokens
-                                     // beside 15 decodes; 0.06: 65 and 41)
+                                     // (0: 78 us for 128 users behind three prefixes, 77 for a chunk of 256 tokens
+                                     // beside 15 decodes of 200 to 4000 keys; 0.06: 67 and 70)
 constexpr int kSharedNew = 16;       // new tokens a sequence up to which a group is shared
 constexpr int kTiledSlots = 512;     // workgroups of the tiled kernel that run at once
 

@@ -14,7 +14,7 @@
 // 51 us (54 with their half lines past the caches).  Between the kernels that
 // write its inputs and read q, 17122 tokens gain the same (368 -> 344 us for all
 // three), 6060 more (153 -> 129), 2015, which the last cache level holds, lose
-// (47 -> 50).  7531 tokens into an 8-bit cache, half turned: 48 us from HBM, 4.9
+// (47 -> 50).  6060 tokens into an 8-bit cache, half turned: 48 us from HBM, 4.9
 // TB/s; 32 single tokens 5 us, launch latency: their heads are dealt over three
 // workgroups each.
 #include "bd_device.h"

@@ -258,8 +258,8 @@ def kv_append(q, k, v, inv_freq, kv: PagedKV, batch: PagedBatch, *, interleaved:
     """Rotate q and k by their positions and store k and v at their places of
     the cache.  q bf16 [T, H, D] (or None), k and v bf16 [T, H_kv, D], token
     strides free (views of a fused projection); inv_freq fp64 [rotary / 2] in
-    radians a position (None: no rotation).  Returns the rotated q (q_out
-    where given; q itself where it is dense: in place)."""
+    radians a position (None: no rotation).  Returns the rotated q: a new
+    tensor, or q_out where given (which may be q itself where it is dense)."""
     kp, ks = _heads(k, "k", (None, kv.n_kv_heads), kv)
     T = k.shape[0]
     vp, vs = _heads(v, "v", (T, kv.n_kv_heads), kv)
