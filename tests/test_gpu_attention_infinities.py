@@ -45,3 +45,17 @@ def test_infinite_values_are_infinite_wherever_the_key_falls(bd, new, ctx, D):
                 s = sum(seen)
                 assert (col.isnan() if np.isnan(s) else col == s).all(), (keys, bad, t, f64(col))
         assert np.isnan(want) == bool(col.isnan().all())
+
+
+@pytest.mark.parametrize("new,ctx", [([1], [0]), ([1], [40]), ([70], [9]), ([200], [300])])
+def test_rows_whose_scores_are_all_minus_infinity(bd, new, ctx):
+    """Keys of -inf against a positive query: such a row is zero, and a row that sees one finite score has its value."""
+    c = Case(new, ctx, 2, 1, 64, 16, seed=44)
+    c.q[:, :, 0] = 1.0
+    c.k[:, 0, :, 0] = -INF
+    assert not bd.attention(c.q, c.kv(bd), c.batch(bd)).any()
+    last = ctx[0] + new[0] - 1                              # the last token's own key, seen by no other
+    pg, sl = int(c.host.table[0, last // 16]), last % 16
+    c.k[pg, 0, sl, 0] = 1.0
+    out = bd.attention(c.q, c.kv(bd), c.batch(bd))
+    assert not out[:-1].any() and torch.equal(out[-1], c.v[pg, :, sl].expand(2, 64))
