@@ -14,6 +14,7 @@
 #include "../../include/bitdelta.h"
 #include "bd_launch.h"
 #include "decoder_launch.h"
+#include "int8_launch.h"
 
 namespace {
 
@@ -735,6 +736,111 @@ bd_status bitdelta_attention(const bd_bf16 *q, int64_t q_stride, int32_t n_heads
     return device(bd::launch_attention(q, q_stride, n_heads, scale, *cache, *batch, out, workspace,
                                        (hipStream_t)stream),
                   "bitdelta_attention");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- bitdelta_int8.h
+
+extern "C" {
+
+bd_status bitdelta_quantize_int8(const void *x, int64_t x_stride, int x_dtype, int64_t m, int64_t d, int8_t *q,
+                                 float *scale, void *stream)
+{
+    if (x_dtype != BD_BF16 && x_dtype != BD_F32)
+        return fail(BD_EINVAL, "x_dtype must be BD_BF16 (0) or BD_F32 (1), got %d", x_dtype);
+    if (m < 0 || m > kMaxGrid)
+        return fail(BD_ESHAPE, "m must be in [0, 2^31) (got %lld)", (long long)m);
+    if (d < 1 || d > BD_INT8_MAX_WIDTH)
+        return fail(BD_ESHAPE, "d must be in [1, %d] (got %lld)", BD_INT8_MAX_WIDTH, (long long)d);
+    if (m == 0)   // an empty tensor has no address
+        return BD_OK;
+    BD_NONNULL(x);
+    BD_NONNULL(q);
+    BD_NONNULL(scale);
+    BD_TRY(check_rows("x", x_stride, d, 1));
+    BD_ALIGNED(x, x_dtype == BD_F32 ? 4 : 2);
+    BD_ALIGNED(scale, 4);
+    return device(bd::launch_quantize_int8(x, x_stride, x_dtype == BD_F32, m, d, q, scale, (hipStream_t)stream),
+                  "bitdelta_quantize_int8");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Extents of a linear over an 8-bit base; n_variants 0: no deltas.
+bd_status check_int8_shape(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in, int64_t y_bytes)
+{
+    if (n_variants < 0 || n_variants > 4096)
+        return fail(BD_EINVAL, "n_variants must be in [0, 4096] (got %d)", n_variants);
+    BD_TRY(check_matrix(d_out, d_in));
+    if (d_in > BD_INT8_MAX_WIDTH)
+        return fail(BD_ESHAPE, "d_in must be at most %d (got %lld)", BD_INT8_MAX_WIDTH, (long long)d_in);
+    if (d_out > (int64_t)1 << 26)   // 512 threads for 16 channels, fewer than 2^32 in all
+        return fail(BD_ESHAPE, "d_out must be at most 2^26 (got %lld)", (long long)d_out);
+    if (m < 0)
+        return fail(BD_ESHAPE, "m must be >= 0 (got %lld)", (long long)m);
+    const int64_t limit = (int64_t(1) << 31) - 1;
+    if (m > limit / d_in || d_out > limit / d_in || m > limit / y_bytes / d_out)
+        return fail(BD_ESHAPE, "q, w and y must each be below 2 GiB (m=%lld, d_out=%lld, d_in=%lld)", (long long)m,
+                    (long long)d_out, (long long)d_in);
+    return BD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bitdelta_linear_int8_workspace(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
+{
+    if (check_int8_shape(m, n_variants, d_out, d_in, 2) != BD_OK || m == 0)
+        return 0;
+    return bd::linear_int8_workspace_bytes(m, n_variants, d_out, d_in);
+}
+
+bd_status bitdelta_linear_int8(const int8_t *q, const float *q_scale, int64_t m, const int8_t *w, const float *w_scale,
+                               const uint8_t *signs, const float *alpha, int alpha_mode, const int32_t *variant_ids,
+                               int32_t n_variants, int64_t d_out, int64_t d_in, void *y, int y_dtype, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    BD_TRY(check_mode(alpha_mode));
+    if (y_dtype != BD_BF16 && y_dtype != BD_F32)
+        return fail(BD_EINVAL, "y_dtype must be BD_BF16 (0) or BD_F32 (1), got %d", y_dtype);
+    if (!signs && (alpha || variant_ids || n_variants != 0))
+        return fail(BD_EINVAL, "alpha, variant_ids and n_variants need signs");
+    if (signs && n_variants < 1)
+        return fail(BD_EINVAL, "signs need n_variants of at least 1 (got %d)", n_variants);
+    if (signs && !variant_ids && n_variants != 1)
+        return fail(BD_EINVAL, "%d variants need variant_ids", n_variants);
+    BD_TRY(check_int8_shape(m, n_variants, d_out, d_in, y_dtype == BD_F32 ? 4 : 2));
+    const size_t need = bitdelta_linear_int8_workspace(m, n_variants, d_out, d_in);
+    if (workspace_bytes < need)
+        return fail(BD_EWORKSPACE, "linear_int8 needs %zu workspace bytes, got %zu", need, workspace_bytes);
+    if (m == 0)
+        return BD_OK;
+    BD_NONNULL(q);
+    BD_NONNULL(q_scale);
+    BD_NONNULL(w);
+    BD_NONNULL(w_scale);
+    BD_NONNULL(y);
+    BD_ALIGNED(q, 16);
+    BD_ALIGNED(w, 16);
+    BD_ALIGNED(y, 16);
+    BD_ALIGNED(q_scale, 4);
+    BD_ALIGNED(w_scale, 4);
+    if (signs) {
+        BD_NONNULL(alpha);
+        BD_ALIGNED(alpha, 4);
+        BD_ALIGNED(variant_ids, 4);
+    }
+    if (need) {
+        BD_NONNULL(workspace);
+        BD_ALIGNED(workspace, 16);
+    }
+    const bd::Int8Args a{q, w, q_scale, w_scale, signs, alpha, variant_ids, y, m, d_out, d_in, n_variants,
+                         alpha_mode == BD_ALPHA_MATRIX, y_dtype == BD_F32};
+    return device(bd::launch_linear_int8(a, workspace, (hipStream_t)stream), "bitdelta_linear_int8");
 }
 
 }  // extern "C"
