@@ -24,7 +24,8 @@ __all__ = ["lib", "lib_path", "BitDeltaError", "compress", "reconstruct", "linea
            "BD_OK", "BD_EINVAL", "BD_ESHAPE", "BD_EALIGN", "BD_EWORKSPACE", "BD_EDEVICE", "BD_EBUSY",
            "BD_CACHE_HIT", "BD_CACHE_MISS", "BD_CACHE_JOINED",
            "BD_BF16", "BD_F32", "BD_ALPHA_ROW", "BD_ALPHA_MATRIX", "EXPORTS",
-           "block_norm", "kv_append", "attention", "PagedKV", "PagedBatch", "quantize_int8", "linear_int8"]
+           "block_norm", "kv_append", "attention", "PagedKV", "PagedBatch", "quantize_int8", "linear_int8",
+           "sample"]
 
 BD_OK, BD_EINVAL, BD_ESHAPE, BD_EALIGN, BD_EWORKSPACE, BD_EDEVICE, BD_EBUSY = range(7)
 BD_CACHE_HIT, BD_CACHE_MISS, BD_CACHE_JOINED = 0, 1, 2
@@ -74,6 +75,10 @@ EXPORTS = {
     "bitdelta_quantize_int8": (_INT, [_P, _I64, _INT, _I64, _I64, _P, _P, _P]),
     "bitdelta_linear_int8_workspace": (_SZ, [_I64, _I32, _I64, _I64]),
     "bitdelta_linear_int8": (_INT, [_P, _P, _I64, _P, _P, _P, _P, _INT, _P, _I32, _I64, _I64, _P, _INT, _P, _SZ, _P]),
+    # include/bitdelta_sample.h
+    "bitdelta_sample_workspace": (_SZ, [_I64, _I64]),
+    "bitdelta_sample": (_INT, [_P, _I64, _INT, _I64, _I64, _P, _P, ctypes.c_float, _P, _I32, _P, ctypes.c_float, _P,
+                               ctypes.c_float, _P, _P, _P, _SZ, _P]),
     # include/bitdelta_cache.h
     "bitdelta_cache_create": (_INT, [_I32, _I32, _I32, _I64, _P, _SZ, _P, _P, _P]),
     "bitdelta_cache_destroy": (None, [_P]),
@@ -484,7 +489,7 @@ class DeltaCache:
 
 # name -> module.  These need torch, which the package itself does without where there is none.
 _MODULES = {**dict.fromkeys(("block_norm", "kv_append", "attention", "PagedKV", "PagedBatch"), "decoder"),
-            **dict.fromkeys(("quantize_int8", "linear_int8"), "int8")}
+            **dict.fromkeys(("quantize_int8", "linear_int8"), "int8"), "sample": "sampling"}
 
 
 def __getattr__(name):

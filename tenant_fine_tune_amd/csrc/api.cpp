@@ -15,6 +15,7 @@
 #include "bd_launch.h"
 #include "decoder_launch.h"
 #include "int8_launch.h"
+#include "sample_launch.h"
 
 namespace {
 
@@ -841,6 +842,54 @@ bd_status bitdelta_linear_int8(const int8_t *q, const float *q_scale, int64_t m,
     const bd::Int8Args a{q, w, q_scale, w_scale, signs, alpha, variant_ids, y, m, d_out, d_in, n_variants,
                          alpha_mode == BD_ALPHA_MATRIX, y_dtype == BD_F32};
     return device(bd::launch_linear_int8(a, workspace, (hipStream_t)stream), "bitdelta_linear_int8");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------ bitdelta_sample.h
+
+extern "C" {
+
+size_t bitdelta_sample_workspace(int64_t m, int64_t vocab)
+{
+    if (m < 1 || m > BD_SAMPLE_MAX_ROWS || vocab < 1 || vocab > BD_SAMPLE_MAX_VOCAB)
+        return 0;
+    return bd::sample_workspace_bytes(m, vocab);
+}
+
+bd_status bitdelta_sample(const void *logits, int64_t logits_stride, int logits_dtype, int64_t m, int64_t vocab,
+                          const float *u, const float *temperature, float temperature_all, const int32_t *top_k,
+                          int32_t top_k_all, const float *top_p, float top_p_all, const float *min_p, float min_p_all,
+                          int32_t *tokens, float *logprobs, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (logits_dtype != BD_BF16 && logits_dtype != BD_F32)
+        return fail(BD_EINVAL, "logits_dtype must be BD_BF16 (0) or BD_F32 (1), got %d", logits_dtype);
+    if (m < 0 || m > BD_SAMPLE_MAX_ROWS)
+        return fail(BD_ESHAPE, "m must be in [0, %d] (got %lld)", BD_SAMPLE_MAX_ROWS, (long long)m);
+    if (vocab < 1 || vocab > BD_SAMPLE_MAX_VOCAB)
+        return fail(BD_ESHAPE, "vocab must be in [1, %d] (got %lld)", BD_SAMPLE_MAX_VOCAB, (long long)vocab);
+    const size_t need = bitdelta_sample_workspace(m, vocab);
+    if (workspace_bytes < need)
+        return fail(BD_EWORKSPACE, "sample needs %zu workspace bytes, got %zu", need, workspace_bytes);
+    if (m == 0)   // an empty tensor has no address
+        return BD_OK;
+    BD_NONNULL(logits);
+    BD_NONNULL(u);
+    BD_NONNULL(tokens);
+    BD_NONNULL(workspace);
+    BD_TRY(check_rows("logits", logits_stride, vocab, 1));
+    BD_ALIGNED(logits, logits_dtype == BD_F32 ? 4 : 2);
+    BD_ALIGNED(u, 4);
+    BD_ALIGNED(temperature, 4);
+    BD_ALIGNED(top_k, 4);
+    BD_ALIGNED(top_p, 4);
+    BD_ALIGNED(min_p, 4);
+    BD_ALIGNED(tokens, 4);
+    BD_ALIGNED(logprobs, 4);
+    BD_ALIGNED(workspace, 16);
+    const bd::SampleArgs a{logits, logits_stride, m, (int32_t)vocab, logits_dtype == BD_F32, u, temperature, top_p, min_p,
+                           top_k, temperature_all, top_p_all, min_p_all, top_k_all, tokens, logprobs};
+    return device(bd::launch_sample(a, workspace, (hipStream_t)stream), "bitdelta_sample");
 }
 
 }  // extern "C"
