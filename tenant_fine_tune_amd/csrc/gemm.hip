@@ -939,14 +939,20 @@ hipError_t grouped_scratch(int32_t **table)
     return hipSuccess;
 }
 
+hipError_t launch_bucket_tokens(const int32_t *ids, int64_t m, int32_t n_variants, int32_t *table, hipStream_t s)
+{
+    hipLaunchKernelGGL(bucket_tokens, dim3(1), dim3(kBucketThreads), 0, s, ids, m, n_variants,
+                       grouped_max_tiles(m, n_variants), table);
+    return hipGetLastError();
+}
+
 hipError_t launch_grouped(const uint16_t *x, int64_t m, const int32_t *ids, int32_t n_variants,
                           const uint16_t *w_base, const uint8_t *signs, const float *alpha,
                           bool per_matrix, int64_t d_out, int64_t d_in, uint16_t *y,
                           int32_t *workspace, hipStream_t s)
 {
     const int64_t T = grouped_max_tiles(m, n_variants);
-    hipLaunchKernelGGL(bucket_tokens, dim3(1), dim3(kBucketThreads), 0, s, ids, m, n_variants, T, workspace);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = launch_bucket_tokens(ids, m, n_variants, workspace, s);
     if (e != hipSuccess)
         return e;
     if (!w8_shape(d_out, d_in))

@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "int8_device.h"
+#include "int8_tiles.h"
 
 namespace bd {
 namespace {
@@ -33,8 +34,10 @@ void int8_stream(Int8Args a)
 
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * 16, K = a.d_in, N = a.d_out, G = K >> 3;
-    const int64_t t0 = (int64_t)blockIdx.y * (16 * T);
+    // blocks of tokens next to one another: they read the same rows of w
+    const unsigned across = (unsigned)((a.m + 16 * T - 1) / (16 * T));
+    const int64_t n0 = (int64_t)(blockIdx.x / across) * 16, K = a.d_in, N = a.d_out, G = K >> 3;
+    const int64_t t0 = (int64_t)(blockIdx.x % across) * (16 * T);
     const int count = (int)(a.m - t0 < 16 * T ? a.m - t0 : 16 * T);
 
     // lane p: the token at place p of the order by variant, and its variant
@@ -241,7 +244,7 @@ void int8_stream(Int8Args a)
 template <int T>
 hipError_t stream(const Int8Args &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.d_out + 15) / 16), (unsigned)((a.m + 16 * T - 1) / (16 * T)));
+    const dim3 grid((unsigned)((a.d_out + 15) / 16 * ((a.m + 16 * T - 1) / (16 * T))));
     const bool odd = a.d_in % 32 != 0 || ((uintptr_t)a.signs & 3) != 0;
     if (!a.signs) {
         if (a.d_in % 16)
@@ -257,10 +260,18 @@ hipError_t stream(const Int8Args &a, hipStream_t s)
 
 }  // namespace
 
-size_t linear_int8_workspace_bytes(int64_t, int32_t, int64_t, int64_t) { return 0; }
+// From this many tokens on the tiles are used.
+constexpr int64_t kTilesFrom = 65;
 
-hipError_t launch_linear_int8(const Int8Args &a, void *, hipStream_t s)
+size_t linear_int8_workspace_bytes(int64_t m, int32_t n_variants, int64_t, int64_t)
 {
+    return m < kTilesFrom ? 0 : int8_tiles_workspace_bytes(m, n_variants);
+}
+
+hipError_t launch_linear_int8(const Int8Args &a, void *workspace, hipStream_t s)
+{
+    if (a.m >= kTilesFrom && int8_tiles_take(a))
+        return launch_int8_tiles(a, workspace, s);
     return a.m <= 16 ? stream<1>(a, s) : a.m <= 32 ? stream<2>(a, s) : stream<4>(a, s);
 }
 
