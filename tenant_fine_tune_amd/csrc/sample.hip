@@ -8,66 +8,79 @@
 //   sample_bins  a part of a row is read once and held in registers: its largest
 //                logit, then for each of 2048 bins the tokens in it and the sum of
 //                their weights.
-//   sample_draw  one workgroup a row adds the parts' bins up, finds the bin of each
-//                border (top-k, top-p, min-p, the draw), and the place within it.
+//   sample_draw  one workgroup a row adds the parts' bins up.  The sums in front of
+//                the bins tell which bins can hold a border (top-k, top-p, min-p, the
+//                draw); the row is read a second time, from the caches, for the
+//                tokens in those, and every border is found among them.  Where they
+//                are too many (nearly flat rows), border by border through smaller bins.
 //
 // Bins are d = 2^e wide, T / 64 < d <= T / 32, at multiples of d, so the parts' bins
 // are the same ones; 2048 of them reach exp(-32) below the part's largest logit, and
-// what lies deeper has no weight.  In a bin with upper edge E the weight relative to
-// it, exp((l - E) / T), is within 1/32 of one; what is missing to one, held in units
-// of 2^-36, and the count share a 64-bit number, so that one LDS addition serves
-// both, and all sums are of whole numbers: exact, in any order, cut in any way.
+// what lies deeper has no weight.  In a bin with lower edge L the weight relative to
+// it, exp((l - L) / T), exceeds one by 1/32 at most; that excess, held in units of
+// 2^-36, and the count share a 64-bit number, so that one LDS addition serves both,
+// and all sums are of whole numbers: exact, in any order, cut in any way.
 #include "bd_device.h"
 #include "sample_launch.h"
 
 namespace bd {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kBinThreads = 1024;            // of sample_bins
 constexpr int kBins = 2048;
-constexpr int kCountShift = 47;              // of a packed bin: below it 65536 tokens' missing weight, each below 2^31
-constexpr uint64_t kMissing = (1ull << kCountShift) - 1;
-constexpr double kOne = 0x1p36;              // weight of a token at its bin's upper edge
-constexpr int kList = 4096;                  // tokens put in order at a time
+constexpr int kCountShift = 47;              // of a packed bin: below it 65536 tokens' excess, each below 2^31
+constexpr uint64_t kExcess = (1ull << kCountShift) - 1;
+constexpr uint32_t kWithoutExponents = 0x9DA1u;   // inverse of 1 + 0x433 * 2^5 of 2^17
+constexpr double kOne = 0x1p36;              // weight of a token at its bin's lower edge
+constexpr int kFew = 128;
 
 typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// Logits as they count: NaN is never drawn, like -inf, and the zeros are equal.
-__device__ __forceinline__ float counted(float l) { return l == l ? l + 0.0f : -INFINITY; }
+// Eight logits as loaded; the ones that do not exist are -inf.
+template <typename T>
+struct Eight;
 
-__device__ __forceinline__ void load8(const uint16_t *p, int n, float *l)
-{
-    if (n == 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4a2 *>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            l[i] = counted(i & 1 ? hi_f32(w[i >> 1]) : lo_f32(w[i >> 1]));
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        l[i] = i < n ? counted(__uint_as_float((uint32_t)p[i] << 16)) : -INFINITY;
-}
-
-__device__ __forceinline__ void load8(const float *p, int n, float *l)
-{
-    if (n == 8) {
-        const u32x4 a = *reinterpret_cast<const u32x4a4 *>(p), b = *reinterpret_cast<const u32x4a4 *>(p + 4);
+template <>
+struct Eight<uint16_t> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const uint16_t *p, int n)
+    {
+        if (n == 8) {
+            w = *reinterpret_cast<const u32x4a2 *>(p);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            l[i] = counted(__uint_as_float(a[i])), l[4 + i] = counted(__uint_as_float(b[i]));
-        return;
+            w[i] = (2 * i < n ? p[2 * i] : 0xFF80u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] : 0xFF80u) << 16;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        l[i] = i < n ? counted(p[i]) : -INFINITY;
-}
+    __device__ __forceinline__ float get(int i) const { return i & 1 ? hi_f32(w[i >> 1]) : lo_f32(w[i >> 1]); }
+};
 
-// Numbers that order as the logits do, and back.
+template <>
+struct Eight<float> {
+    u32x4 a, b;
+    __device__ __forceinline__ void load(const float *p, int n)
+    {
+        if (n == 8) {
+            a = *reinterpret_cast<const u32x4a4 *>(p);
+            b = *reinterpret_cast<const u32x4a4 *>(p + 4);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            (i < 4 ? a : b)[i & 3] = i < n ? __float_as_uint(p[i]) : 0xFF800000u;
+    }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i < 4 ? a[i] : b[i - 4]); }
+};
+
+__device__ __forceinline__ float one_of(const uint16_t *p, int i) { return __uint_as_float((uint32_t)p[i] << 16); }
+__device__ __forceinline__ float one_of(const float *p, int i) { return p[i]; }
+
+// Numbers that order as the logits do (the zeros alike), and back.
 __device__ __forceinline__ uint32_t key_of(float l)
 {
-    const uint32_t b = __float_as_uint(l);
+    const uint32_t b = __float_as_uint(l + 0.0f);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float logit_of(uint32_t k)
@@ -75,55 +88,57 @@ __device__ __forceinline__ float logit_of(uint32_t k)
     return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
 }
 
-// The bins of a row, counted downwards from the one of `top`.
+// The bins of a row, counted downwards from the one of its largest logit.
 struct Scale {
-    double to_bin, width, top_bin;    // 1/d, d/T, floor(top / d)
-    float top;
-    bool flat, drawn_max;             // T = +inf: all tokens of weight one; top = +inf: those alone
+    double c1, c2, c3, c4;       // excess(f) = f (c1 + f (c2 + f (c3 + f c4))), f = place in the bin
+    double t;
+    float top, top_bin;          // largest logit, floor(top / d)
+    int shift;                   // d = 2^-shift
+    bool alone;                  // only tokens at `top` have a weight (top = +inf, or so far above T that its neighbours have none)
+    bool flat;                   // T = +inf: every token has weight one
 
     __device__ __forceinline__ void set(float temperature, float largest)
     {
         top = largest;
+        t = temperature;
         flat = temperature == INFINITY;
-        drawn_max = largest == INFINITY;
         int e;
-        frexp((double)temperature, &e);                       // T in [2^(e-1), 2^e)
-        to_bin = flat ? 0.0 : ldexp(1.0, 6 - e);              // d = 2^(e-6): T / 64 < d <= T / 32
-        width = flat ? 0.0 : ldexp(1.0, e - 6) / (double)temperature;
-        top_bin = drawn_max || flat ? 0.0 : floor((double)largest * to_bin);
+        frexp(t, &e);                             // T in [2^(e-1), 2^e)
+        shift = flat ? -2000 : 6 - e;             // d = 2^(e-6): T / 64 < d <= T / 32
+        // from 2^36 d on the next smaller logits are 2048 bins away
+        alone = largest == INFINITY || fabs(ldexp((double)largest, shift)) >= 0x1p36;
+        top_bin = floorf(ldexpf(largest, shift));
+        // exp(x) - 1 for 0 <= x <= 1/32, as x times a polynomial through its four Chebyshev points: within 2^-38
+        const double w = flat ? 0.0 : ldexp(1.0, -shift) / t;
+        c1 = w * 0x1.ffffffff76092p-1 * kOne;
+        c2 = w * w * 0x1.00000227c482ap-1 * kOne;
+        c3 = w * w * w * 0x1.554ff31ff6e04p-3 * kOne;
+        c4 = w * w * w * w * 0x1.59a176b303773p-5 * kOne;
     }
-    // Bin of l (kBins: none), and how far below the bin's upper edge it lies, in bins.
-    __device__ __forceinline__ int bin(float l, double &below) const
+    // Bin of l as a number, at least kBins or NaN where it has none (l NaN or -inf).
+    __device__ __forceinline__ float bin(float l) const
     {
-        below = 0.0;
-        if (l == -INFINITY)
-            return kBins;
-        if (drawn_max)
-            return l == INFINITY ? 0 : kBins;
-        if (flat)
-            return 0;
-        const double a = (double)l * to_bin, b = floor(a), rel = top_bin - b;
-        below = b + 1.0 - a;
-        return rel < kBins ? (int)rel : kBins;
+        if (alone)
+            return l == top ? 0.0f : INFINITY;
+        return top_bin - floorf(ldexpf(l, shift));
     }
-    // 1 - exp(-x), x <= 1/32, in units of 2^-36: the series to x^6 is within 2^-47
-    __device__ __forceinline__ uint64_t missing(double below) const
+    // The excess of the logit a / to_bin in the low 47 bits of a double, and a count
+    // of one above it: the sum 2^52 + 2^47 + excess is whole, so its bits are those
+    // numbers under the exponent's.
+    __device__ __forceinline__ uint64_t raw_excess(float a) const
     {
-        const double x = below * width;
-        double s = fma(x, -1.0 / 720.0, 1.0 / 120.0);
-        s = fma(x, s, -1.0 / 24.0);
-        s = fma(x, s, 1.0 / 6.0);
-        s = fma(x, s, -0.5);
-        s = fma(x, s, 1.0);
-        // adding 2^52 leaves the whole number in the low bits
-        return (uint64_t)__double_as_longlong(fma(x * s, kOne, 0x1p52)) & kMissing;
+        const double f = __builtin_amdgcn_fract((double)a);
+        return (uint64_t)__double_as_longlong(fma(f, fma(f, fma(f, fma(f, c4, c3), c2), c1), 0x1p52 + 0x1p47));
     }
-    // weight of the upper edge of bin b, relative to the largest logit
-    __device__ __forceinline__ double edge(int b, double temperature) const
+    __device__ __forceinline__ uint64_t weight(float l) const
     {
-        if (drawn_max || flat)
-            return 1.0;
-        return exp(((top_bin - b + 1.0) / to_bin - (double)top) / temperature);
+        return (uint64_t)kOne + (alone ? 0 : raw_excess(ldexpf(l, shift)) & kExcess);
+    }
+    // lower edge of a bin, as a logit, and its weight relative to the largest logit
+    __device__ __forceinline__ double edge(int b) const { return ldexp((double)top_bin - b, -shift); }
+    __device__ __forceinline__ double edge_weight(int b) const
+    {
+        return alone || flat ? 1.0 : exp((edge(b) - (double)top) / t);
     }
 };
 
@@ -148,77 +163,93 @@ __device__ __forceinline__ float wave_max(float v)
 
 // G groups of eight logits a thread.
 template <int G, typename T>
-__global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs a, Part *__restrict__ parts, int32_t splits)
+__global__ __launch_bounds__(kBinThreads)
+void sample_bins(SampleArgs a, Part *__restrict__ parts, int32_t splits)
 {
     __shared__ uint64_t bins[kBins];
-    __shared__ float tops[kThreads / 64];
+    __shared__ float tops[kBinThreads / 64];
     __shared__ int32_t first;
     const int64_t row = blockIdx.x / (unsigned)splits;
     const int split = blockIdx.x % (unsigned)splits;
     const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-    const int at0 = split * (G * 8 * kThreads) + threadIdx.x * 8;
-    float l[G][8];
+    const int at0 = split * (G * 8 * kBinThreads) + threadIdx.x * 8;
+    Eight<T> l[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const int at = at0 + g * 8 * kThreads;
-        load8(p + at, min(max(a.vocab - at, 0), 8), l[g]);
+        const int at = at0 + g * 8 * kBinThreads;
+        l[g].load(p + at, min(max(a.vocab - at, 0), 8));
     }
     const float t = a.temperature ? a.temperature[row] : a.temperature_all;
-    for (int i = threadIdx.x; i < kBins; i += kThreads)
+    for (int i = threadIdx.x; i < kBins; i += kBinThreads)
         bins[i] = 0;
     if (threadIdx.x == 0)
         first = 0x7FFFFFFF;
-    float top = -INFINITY;
+    float top = -INFINITY;       // a maximum passes NaN over
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            top = fmaxf(top, l[g][i]);
+            top = fmaxf(top, l[g].get(i));
     top = wave_max(top);
     if ((threadIdx.x & 63) == 0)
         tops[threadIdx.x >> 6] = top;
     __syncthreads();
-    top = wave_max(tops[threadIdx.x & (kThreads / 64 - 1)]);
+    top = wave_max(tops[threadIdx.x & (kBinThreads / 64 - 1)]);
 
     Part &out = parts[blockIdx.x];
+    if (threadIdx.x == 0)
+        out.top = top;
     if (greedy(t)) {
         int at = 0x7FFFFFFF;
 #pragma unroll
         for (int g = G - 1; g >= 0; --g)
 #pragma unroll
             for (int i = 7; i >= 0; --i)
-                if (l[g][i] == top)
-                    at = at0 + g * 8 * kThreads + i;
+                if (l[g].get(i) == top)
+                    at = at0 + g * 8 * kBinThreads + i;
         if (at != 0x7FFFFFFF)
             atomicMin(&first, at);
         __syncthreads();
-        if (threadIdx.x == 0) {
-            out.top = top;
+        if (threadIdx.x == 0)
             out.first = first;
-        }
         return;
     }
     Scale s;
     s.set(t, top);
-    if (top != -INFINITY)
+    if (s.alone) {
+        int n = 0;
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
+            for (int i = 0; i < 8; ++i)
+                n += l[g].get(i) == top;
+        if (n)
+            atomicAdd((unsigned long long *)&bins[0], (unsigned long long)n << kCountShift);
+    } else {
+        const float first_byte = 8.0f * s.top_bin;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
             for (int i = 0; i < 8; ++i) {
-                double below;
-                const int b = s.bin(l[g][i], below);
-                if (b < kBins)
-                    atomicAdd((unsigned long long *)&bins[b], (1ull << kCountShift) | s.missing(below));
+                const float a = ldexpf(l[g].get(i), s.shift), at = fmaf(floorf(a), -8.0f, first_byte);
+                if (at < 8.0f * kBins)
+                    atomicAdd((unsigned long long *)((uint8_t *)bins + (int)at), (unsigned long long)s.raw_excess(a));
             }
+            __builtin_amdgcn_sched_barrier(0);      // one group's temporaries at a time
+        }
+    }
     __syncthreads();
-    if (threadIdx.x == 0)
-        out.top = top;
-    for (int i = threadIdx.x; i < kBins; i += kThreads)
-        out.bins[i] = bins[i];
+    for (int i = threadIdx.x; i < kBins; i += kBinThreads) {
+        // n exponents, 0x433 from bit 52 on, are in the sum too: the bits from the
+        // count's on are n (1 + 0x433 * 2^5) of 2^17, which an odd factor takes back
+        const uint64_t v = bins[i];
+        const uint32_t n = s.alone ? (uint32_t)(v >> kCountShift) : (uint32_t)(v >> kCountShift) * kWithoutExponents & 0x1FFFFu;
+        out.bins[i] = (uint64_t)n << kCountShift | (v & kExcess);
+    }
 }
 
 // Sum of v over the threads before this one; `total` over all of them.
-template <typename V>
+template <int TH, typename V>
 __device__ __forceinline__ V scan(V v, V *part, V &total)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -235,231 +266,376 @@ __device__ __forceinline__ V scan(V v, V *part, V &total)
     V before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
+    for (int w = 0; w < TH / 64; ++w) {
         const V x = part[w];
         before += w < wave ? x : V(0);
         total += x;
     }
-    return before + s - v;
+    s = __shfl_up(s, 1);
+    return lane ? before + s : before;
+}
+
+// The first of n <= 4096 places that is right, n - 1 if no other is: `right` turns
+// from false to true once.  All lanes of a wave look at places 64 apart, then at those between.
+template <typename F>
+__device__ __forceinline__ int first_of(int n, F right)
+{
+    const int lane = threadIdx.x & 63;
+    const int at = min(lane * 64 + 63, n - 1);
+    const uint64_t far = __ballot(right(at));
+    const int from = far ? (int)__builtin_ctzll(far) * 64 : 63 * 64;
+    const uint64_t near = __ballot(right(min(from + lane, n - 1)));
+    return min(near ? from + (int)__builtin_ctzll(near) : n - 1, n - 1);
 }
 
 // What is looked for in a bin, in the order of its tokens: the first one with at
 // least `count` tokens and `weight` of their weights (whole numbers, both from the
-// bin's beginning, the token included).
+// bin's beginning, the token included), or the last one.
 struct Query {
     uint32_t count;
     uint64_t weight;
 };
 struct Found {
-    int32_t token;
-    uint32_t key;
+    uint64_t entry;        // ~key and token, as they stand in the list
     uint64_t weight;       // from the bin's beginning, the token included
 };
 
-template <typename T>
+// Ranges of bins, each an interval of the sums in front of the bins.
+struct Ranges {
+    int lo[4], hi[4], n, read;
+    float from[4], to[4];    // logits
+};
+
+// TH threads a row.
+template <int TH, typename T>
 struct Draw {
-    // LDS
+    // tokens put in order at a time: as many as LDS holds for one workgroup of 1024 or two of 512 a CU
+    static constexpr int kList = TH == 1024 ? 4096 : 3072;
+    static constexpr int kPicked = 2 * kList;
+
     struct Shared {
-        uint64_t list[kList];
-        uint32_t counts[kBins];
-        uint64_t sums[kBins];
-        double part_d[kThreads / 64];
-        unsigned long long part_u[kThreads / 64];
-        uint32_t part_c[kThreads / 64];
-        uint32_t n, klo, khi;
-        int32_t token, bin;
-        uint64_t weight;
-        double before;
+        uint64_t work[2 * kList];        // the list and its sums; smaller bins
+        double wpre[kBins + 1];          // weights and tokens in front of a bin
+        uint32_t cpre[kBins + 1];
+        double part_d[TH / 64];
+        unsigned long long part_u[TH / 64];
+        uint32_t part_c[TH / 64];
+        uint32_t guess[kList / 2];       // two 16-bit numbers each
+        uint32_t n, passed;
+        int32_t hit;
+        uint32_t hit_n, hit_count;
+        uint64_t hit_weight, entry;
+        Ranges r;
+        uint32_t listed;
+        int32_t least_lo, least_hi;
     };
     Shared &sh;
     const SampleArgs &a;
     const T *row;
+    uint64_t *list, *upto;               // ~key and index of tokens, in order once order() was called; their weights added up
     Scale s;
 
-    // Calls f(token, logit) for every token of bin b whose key is within [klo, khi].
+    // Calls f(token, logit) for every token whose logit is within [lo, hi].
     template <typename F>
-    __device__ __forceinline__ void each(int b, uint32_t klo, uint32_t khi, F f)
+    __device__ __forceinline__ void each(float lo, float hi, F f)
     {
-        for (int at = threadIdx.x * 8; at < a.vocab; at += kThreads * 8) {
-            float l[8];
-            load8(row + at, min(a.vocab - at, 8), l);
+#pragma unroll 1
+        for (int at = threadIdx.x * 8; at < a.vocab; at += TH * 8) {
+            Eight<T> l;
+            l.load(row + at, min(a.vocab - at, 8));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                double below;
-                const uint32_t k = key_of(l[i]);
-                if (k >= klo && k <= khi && s.bin(l[i], below) == b)
-                    f(at + i, l[i], k, below);
+                const float x = l.get(i);
+                if (x >= lo && x <= hi)
+                    f(at + i, x);
             }
         }
     }
 
-    // The token of bin b that the query asks for; n of them are there.
-    __device__ Found find(int b, uint32_t n, Query q)
+    // Puts the tokens whose logits are within one of N ranges [lo, hi] into
+    // picked(), in any order, as far as they fit; sh.n counts them.
+    template <int N>
+    __device__ __forceinline__ void pick(const float *lo, const float *hi)
     {
-        // keys of the bin's edges, one step to the outside of their roundings
-        uint32_t klo = 0, khi = 0xFFFFFFFFu;
-        if (!s.flat && !s.drawn_max) {
-            const float lo = (float)((s.top_bin - b) / s.to_bin), hi = (float)((s.top_bin - b + 1.0) / s.to_bin);
-            klo = key_of(counted(lo)) - 1;
-            khi = key_of(counted(hi)) + 1;
+        constexpr int kBatch = 4, kSpan = TH * 8;     // loads on their way together
+        float from[N], to[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            from[r] = lo[r], to[r] = hi[r];
+#pragma unroll 1
+        for (int base = threadIdx.x * 8; base < a.vocab; base += kBatch * kSpan) {
+            Eight<T> l[kBatch];
+#pragma unroll
+            for (int g = 0; g < kBatch; ++g)
+                l[g].load(row + base + g * kSpan, min(max(a.vocab - base - g * kSpan, 0), 8));
+            uint32_t hits = 0;
+#pragma unroll
+            for (int i = 0; i < kBatch * 8; ++i) {
+                const float x = l[i >> 3].get(i & 7);
+                bool hit = false;
+#pragma unroll
+                for (int r = 0; r < N; ++r)
+                    hit |= x >= from[r] && x <= to[r];
+                hits = hits + hits + (hit ? 1u : 0u);
+            }
+            while (hits) {
+                const int i = __builtin_clz(hits);
+                hits &= ~(0x80000000u >> i);
+                const uint32_t n = atomicAdd(&sh.n, 1u);
+                if (n < kPicked)
+                    picked()[n] = (uint32_t)(base + (i >> 3) * kSpan + (i & 7));
+            }
         }
+    }
+    __device__ __forceinline__ uint32_t *picked() const { return reinterpret_cast<uint32_t *>(upto); }
+
+    // Logits that the bins lo .. hi hold.
+    __device__ __forceinline__ void span(int lo, int hi, float &from, float &to) const
+    {
+        if (s.alone) {
+            from = to = s.top;
+            return;
+        }
+        from = -__FLT_MAX__;
+        to = s.top;
+        if (s.flat)
+            return;
+        // the first logit from the lower edge on, the last one in front of the upper one
+        const double e0 = s.edge(hi), e1 = s.edge(lo - 1);
+        const float f0 = (float)e0, f1 = (float)e1;
+        from = fmaxf((double)f0 < e0 ? logit_of(key_of(f0) + 1) : f0, from);
+        if (lo > 0)
+            to = fminf((double)f1 >= e1 ? logit_of(key_of(f1) - 1) : f1, to);
+    }
+
+    // Puts the list's n entries in order and adds their weights up.  Where an entry
+    // will stand is guessed from its place in its bin (r: the list's bins; none: all
+    // entries are of one bin, with keys from klo to khi); entries of one guess count
+    // those before them among themselves.
+    __device__ void order(int n, const Ranges *r, uint32_t klo, uint32_t khi)
+    {
+        if (n <= kFew) {
+            uint64_t e = 0;
+            int before = 0;
+            if ((int)threadIdx.x < n) {
+                e = list[threadIdx.x];
+                for (int i = 0; i < n; ++i)
+                    before += list[i] < e;
+            }
+            __syncthreads();
+            if ((int)threadIdx.x < n)
+                list[before] = e;
+        } else {
+            constexpr int per = kList / TH;
+            for (int i = threadIdx.x; i < kList / 2; i += TH)
+                sh.guess[i] = 0;
+            __syncthreads();
+            uint64_t e[per];
+            uint32_t at[per], place[per];
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                const int j = threadIdx.x + i * TH;
+                at[i] = place[i] = 0;
+                e[i] = ~0ull;
+                if (j < n) {
+                    e[i] = list[j];
+                    const uint32_t key = ~(uint32_t)(e[i] >> 32);
+                    if (r) {
+                        const float l = logit_of(key);
+                        const int b = (int)s.bin(l);
+                        const uint32_t held = sh.cpre[b + 1] - sh.cpre[b];
+                        for (int q = 0; q < r->n; ++q)
+                            at[i] += sh.cpre[min(max(b, r->lo[q]), r->hi[q] + 1)] - sh.cpre[r->lo[q]];
+                        // equal logits of 16 bits, of which a bin holds few different ones, are spread by their
+                        // index over the step below the next larger logit; of one weight for all (flat) the bin
+                        // says nothing of a logit's place
+                        const int step = (int)(__float_as_uint(l) >> 23 & 255) - 134 + s.shift;
+                        const float u = s.flat ? 0.0f : s.alone ? 1.0f : sizeof(T) == 2 ? fminf(ldexpf(1.0f, step), 1.0f) : 0.0f;
+                        const float f = s.flat ? 1.0f : s.alone ? 0.0f : __builtin_amdgcn_fractf(ldexpf(l, s.shift));
+                        const float below = 1.0f - f - u + u * (float)(uint32_t)e[i] / (float)a.vocab;
+                        at[i] += min((uint32_t)(fmaxf(below, 0.0f) * (float)held), held - 1);
+                    } else {
+                        at[i] = (uint32_t)(((uint64_t)(khi - key) * (uint32_t)n) / ((uint64_t)(khi - klo) + 1));
+                    }
+                    const int half = 16 * (at[i] & 1);
+                    place[i] = atomicAdd(&sh.guess[at[i] >> 1], 1u << half) >> half & 0xFFFFu;
+                }
+            }
+            __syncthreads();
+            uint32_t have[per], mine = 0, all;
+            uint16_t *guess = reinterpret_cast<uint16_t *>(sh.guess);
+#pragma unroll
+            for (int i = 0; i < per; ++i)
+                mine += have[i] = guess[threadIdx.x * per + i];
+            uint32_t before = scan<TH>(mine, sh.part_c, all);
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                guess[threadIdx.x * per + i] = (uint16_t)before;
+                before += have[i];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < per; ++i)
+                if (threadIdx.x + i * TH < (unsigned)n)
+                    upto[guess[at[i]] + place[i]] = e[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < per; ++i)
+                if (threadIdx.x + i * TH < (unsigned)n) {
+                    const int from = guess[at[i]], to = at[i] + 1 < (unsigned)kList ? (int)guess[at[i] + 1] : n;
+                    int rank = from;
+                    for (int j = from; j < to; ++j)
+                        rank += upto[j] < e[i];
+                    list[rank] = e[i];
+                }
+        }
+        __syncthreads();
+        constexpr int per = kList / TH;
+        const int from = threadIdx.x * per;
+        unsigned long long w[per], mine = 0, all;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            w[i] = from + i < n ? s.weight(logit_of(~(uint32_t)(list[from + i] >> 32))) : 0;
+            mine += w[i];
+        }
+        uint64_t sum = scan<TH>(mine, sh.part_u, all);
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            sum += w[i];
+            upto[from + i] = sum;
+        }
+        __syncthreads();
+    }
+
+    // The query's token among the list's entries from .. from + n - 1, which are in
+    // order, with count0 tokens and weight0 in front of them.
+    __device__ __forceinline__ Found among(int from, int n, uint32_t count0, uint64_t weight0, Query q) const
+    {
+        const uint64_t base = from ? upto[from - 1] : 0;
+        // the last one has what is asked for
+        const int at = first_of(n, [&](int i) { return count0 + i + 1 >= q.count && weight0 + upto[from + i] - base >= q.weight; });
+        return {list[from + at], weight0 + upto[from + at] - base};
+    }
+
+    // The query's token of bin b, which holds n, however many they are.
+    __device__ Found search(int b, uint32_t n, Query q)
+    {
+        float from, to;
+        span(b, b, from, to);
+        uint32_t klo = key_of(from), khi = key_of(to);
         uint32_t count0 = 0;         // tokens and weight of the bin in front of [klo, khi]
         uint64_t weight0 = 0;
         while (n > kList && klo < khi) {
-            // too many to put in order: 2048 smaller bins over the keys, from the largest on
+            // 2048 smaller bins over the keys, from the largest on
             int shift = 0;
             while ((khi - klo) >> shift >= kBins)
                 ++shift;
-            uint32_t *counts = reinterpret_cast<uint32_t *>(sh.list);
-            uint64_t *sums = sh.list + kBins / 2;
+            static_assert(kBins / 2 + kBins <= 2 * kList, "counts and sums");
+            uint32_t *counts = reinterpret_cast<uint32_t *>(sh.work);
+            uint64_t *sums = sh.work + kBins / 2;
             __syncthreads();
-            for (int i = threadIdx.x; i < kBins; i += kThreads)
+            for (int i = threadIdx.x; i < kBins; i += TH)
                 counts[i] = 0, sums[i] = 0;
             __syncthreads();
-            each(b, klo, khi, [&](int, float, uint32_t k, double below) {
-                atomicAdd(&counts[(khi - k) >> shift], 1u);
-                atomicAdd((unsigned long long *)&sums[(khi - k) >> shift], (unsigned long long)((uint64_t)kOne - s.missing(below)));
+            each(logit_of(klo), logit_of(khi), [&](int, float x) {
+                if (s.bin(x) == b) {
+                    const uint32_t i = (khi - key_of(x)) >> shift;
+                    atomicAdd(&counts[i], 1u);
+                    atomicAdd((unsigned long long *)&sums[i], (unsigned long long)s.weight(x));
+                }
             });
             __syncthreads();
-            const int i0 = threadIdx.x * (kBins / kThreads);
+            constexpr int per = kBins / TH;
+            const int i0 = threadIdx.x * per;
             uint32_t c = 0, call;
             unsigned long long w = 0, wall;
-            for (int i = 0; i < kBins / kThreads; ++i)
+#pragma unroll
+            for (int i = 0; i < per; ++i)
                 c += counts[i0 + i], w += sums[i0 + i];
-            uint32_t cs = count0 + scan(c, sh.part_c, call);
-            unsigned long long wsum = weight0 + scan(w, sh.part_u, wall);
-            if (threadIdx.x == 0)
-                sh.bin = -1;
-            __syncthreads();
-            for (int i = 0; i < kBins / kThreads; ++i) {
+            uint32_t cs = count0 + scan<TH>(c, sh.part_c, call);
+            uint64_t wsum = weight0 + scan<TH>(w, sh.part_u, wall);
+            q.weight = min(q.weight, weight0 + (uint64_t)wall);      // roundings may ask for more than there is
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
                 const uint32_t cn = counts[i0 + i];
                 const uint64_t wn = sums[i0 + i];
-                if (cn && (cs < q.count || wsum < q.weight) && cs + cn >= q.count && wsum + wn >= q.weight) {
-                    sh.bin = i0 + i;
-                    sh.n = cn;
-                    sh.klo = cs;
-                    sh.weight = wsum;
+                if ((cs < q.count || wsum < q.weight) && cs + cn >= q.count && wsum + wn >= q.weight) {
+                    sh.hit = i0 + i;
+                    sh.hit_n = cn;
+                    sh.hit_count = cs;
+                    sh.hit_weight = wsum;
                 }
                 cs += cn;
                 wsum += wn;
             }
             __syncthreads();
-            const int hit = sh.bin;
-            n = sh.n, count0 = sh.klo, weight0 = sh.weight;
-            khi = khi - ((uint32_t)hit << shift);
+            n = sh.hit_n, count0 = sh.hit_count, weight0 = sh.hit_weight;
+            khi -= (uint32_t)sh.hit << shift;
             const uint32_t span = (1u << shift) - 1;
             klo = khi - klo > span ? khi - span : klo;
             __syncthreads();
         }
         if (n > kList) {
             // equal logits alone: the one at its place among them, by index
-            const uint64_t one = (uint64_t)kOne;
-            double below;
-            s.bin(logit_of(khi), below);
-            const uint64_t w = one - s.missing(below);
+            const float l = logit_of(khi);
+            const uint64_t w = s.weight(l);
             uint64_t need = q.count > count0 ? q.count - count0 : 1;
             if (q.weight > weight0) {
                 const uint64_t by_weight = (q.weight - weight0 + w - 1) / w;
-                need = by_weight > need ? by_weight : need;
+                need = min(by_weight > need ? by_weight : need, (uint64_t)n);
             }
             // each thread's share is a stretch of the row here
-            const int per = (a.vocab + kThreads - 1) / kThreads, from = threadIdx.x * per;
-            const int to = min(from + per, a.vocab);
-            const float l = logit_of(khi);
+            const int per = (a.vocab + TH - 1) / TH, first = min((int)threadIdx.x * per, a.vocab);
+            const int last = min(first + per, a.vocab);
             uint32_t mine = 0, all;
-            for (int i = from; i < to; ++i)
-                mine += one_of(i) == l;
-            uint32_t before = scan(mine, sh.part_c, all);
+            for (int i = first; i < last; ++i)
+                mine += one_of(row, i) == l;
+            uint32_t before = scan<TH>(mine, sh.part_c, all);
             if (before < need && before + mine >= need)
-                for (int i = from; i < to; ++i)
-                    if (one_of(i) == l && ++before == need)
-                        sh.token = i;
+                for (int i = first; i < last; ++i)
+                    if (one_of(row, i) == l && ++before == need)
+                        sh.entry = (uint64_t)~khi << 32 | (uint32_t)i;
             __syncthreads();
-            return {sh.token, khi, weight0 + need * w};
+            const Found f{sh.entry, weight0 + need * w};
+            __syncthreads();
+            return f;
         }
         if (threadIdx.x == 0)
             sh.n = 0;
         __syncthreads();
-        each(b, klo, khi, [&](int at, float, uint32_t k, double) {
-            const uint32_t i = atomicAdd(&sh.n, 1u);
-            if (i < kList)
-                sh.list[i] = (uint64_t)~k << 32 | (uint32_t)at;
+        each(logit_of(klo), logit_of(khi), [&](int at, float x) {
+            if (s.bin(x) == b)
+                list[min(atomicAdd(&sh.n, 1u), (uint32_t)kList - 1)] = (uint64_t)~key_of(x) << 32 | (uint32_t)at;
         });
         __syncthreads();
-        const int held = min(sh.n, (uint32_t)kList);
-        int size = 2;
-        while (size < held)
-            size *= 2;
-        for (int i = held + threadIdx.x; i < size; i += kThreads)
-            sh.list[i] = ~0ull;
-        for (int k = 2; k <= size; k *= 2)
-            for (int j = k / 2; j > 0; j /= 2) {
-                __syncthreads();
-                for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-                    const int x = (i / j) * 2 * j + i % j, y = x + j;
-                    const uint64_t p = sh.list[x], r = sh.list[y];
-                    if ((p > r) == ((x & k) == 0))
-                        sh.list[x] = r, sh.list[y] = p;
-                }
-            }
-        __syncthreads();
-        constexpr int per = kList / kThreads;
-        const int from = threadIdx.x * per;
-        unsigned long long w[per], mine = 0, all;
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-            w[i] = 0;
-            if (from + i < held) {
-                double below;
-                s.bin(logit_of(~(uint32_t)(sh.list[from + i] >> 32)), below);
-                w[i] = (uint64_t)kOne - s.missing(below);
-            }
-            mine += w[i];
-        }
-        uint64_t sum = weight0 + scan(mine, sh.part_u, all);
-        if (threadIdx.x == 0) {
-            // roundings of the border's place may ask for a little more than there is: the last one then
-            sh.token = (int32_t)sh.list[held - 1];
-            sh.klo = ~(uint32_t)(sh.list[held - 1] >> 32);
-            sh.weight = weight0 + all;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-            const bool before = count0 + from + i < q.count || sum < q.weight;
-            sum += w[i];
-            if (from + i < held && before && count0 + from + i + 1 >= q.count && sum >= q.weight) {
-                sh.token = (int32_t)sh.list[from + i];
-                sh.klo = ~(uint32_t)(sh.list[from + i] >> 32);
-                sh.weight = sum;
-            }
-        }
-        __syncthreads();
-        const Found f{sh.token, sh.klo, sh.weight};
+        order((int)n, nullptr, klo, khi);
+        const Found f = among(0, (int)n, count0, weight0, q);
         __syncthreads();
         return f;
     }
-
-    __device__ __forceinline__ float one_of(int i) const
-    {
-        if constexpr (sizeof(T) == 2)
-            return counted(__uint_as_float((uint32_t)row[i] << 16));
-        else
-            return counted(row[i]);
-    }
 };
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
+// A border: the last kept token, or the one drawn.
+struct Border {
+    double weight;       // of the tokens up to it and with it
+    int bin;
+    Found f;             // within the bin; its entry only where it is looked for
+};
+
+template <int TH, typename T>
+__global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
 {
-    __shared__ typename Draw<T>::Shared sh;
+    constexpr int kList = Draw<TH, T>::kList;
+    __shared__ typename Draw<TH, T>::Shared sh;
     const int64_t row = blockIdx.x;
     parts += row * splits;
-    const double t = a.temperature ? a.temperature[row] : a.temperature_all;
+    const float t = a.temperature ? a.temperature[row] : a.temperature_all;
     float top = -INFINITY;
-    for (int i = 0; i < splits; ++i)
+    for (int i = threadIdx.x & 63; i < splits; i += 64)
         top = fmaxf(top, parts[i].top);
-    if (top == -INFINITY || greedy((float)t)) {
+    top = wave_max(top);
+    if (top == -INFINITY || greedy(t)) {
         if (threadIdx.x == 0) {
             int32_t first = -1;
             for (int i = splits - 1; i >= 0 && top != -INFINITY; --i)
@@ -471,182 +647,324 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleArgs a, const Part
         }
         return;
     }
-    Draw<T> d{sh, a, static_cast<const T *>(a.logits) + row * a.stride, {}};
+    Draw<TH, T> d{sh, a, static_cast<const T *>(a.logits) + row * a.stride, sh.work, sh.work + kList, {}};
     Scale &s = d.s;
-    s.set((float)t, top);
+    s.set(t, top);
 
     // the row's bins, and the sums of counts and weights in front of them
-    constexpr int per = kBins / kThreads;
+    constexpr int per = kBins / TH;
     const int b0 = threadIdx.x * per;
-    uint32_t count[per], counts = 0, all;
+    uint64_t count[per], excess[per];
+#pragma unroll
+    for (int i = 0; i < per; ++i)
+        count[i] = excess[i] = 0;
+    constexpr int kTogether = 4;         // parts whose loads are on their way together
+    for (int p = 0; p < splits; p += kTogether) {
+        float first[kTogether];
+        uint64_t v[kTogether][per];
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+            first[q] = p + q < splits ? s.bin(parts[p + q].top) : INFINITY;      // the part's first bin among the row's
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                v[q][i] = 0;
+                if (first[q] <= (float)(b0 + i))
+                    v[q][i] = parts[p + q].bins[b0 + i - (int)first[q]];
+            }
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                count[i] += v[q][i] >> kCountShift;
+                excess[i] += v[q][i] & kExcess;
+            }
+    }
+    uint32_t counts = 0, all;
     double weight[per], weights = 0, total;
 #pragma unroll
     for (int i = 0; i < per; ++i) {
-        uint64_t n = 0, missing = 0;
-        for (int p = 0; p < splits; ++p) {
-            double below;
-            const float largest = parts[p].top;
-            // the part's first bin among the row's
-            const int shift = s.bin(largest, below), b = b0 + i - shift;
-            if (b >= 0 && b < kBins && shift < kBins) {
-                const uint64_t v = parts[p].bins[b];
-                n += v >> kCountShift;
-                missing += v & kMissing;
-            }
-        }
-        count[i] = (uint32_t)n;
-        sh.counts[b0 + i] = count[i];
-        sh.sums[b0 + i] = n * (uint64_t)kOne - missing;
-        weight[i] = n ? (double)sh.sums[b0 + i] * (1.0 / kOne) * s.edge(b0 + i, t) : 0.0;
-        counts += count[i];
+        const uint64_t w = count[i] * (uint64_t)kOne + excess[i];
+        weight[i] = w ? (double)w * (1.0 / kOne) * s.edge_weight(b0 + i) : 0.0;
+        counts += (uint32_t)count[i];
         weights += weight[i];
     }
-    const uint32_t cbefore = scan(counts, sh.part_c, all);
-    const double wbefore = scan(weights, sh.part_d, total);
+    uint32_t cs = scan<TH>(counts, sh.part_c, all);
+    double ws = scan<TH>(weights, sh.part_d, total);
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+        sh.cpre[b0 + i] = cs;
+        sh.wpre[b0 + i] = ws;
+        cs += (uint32_t)count[i];
+        ws += weight[i];
+    }
+    if (threadIdx.x == TH - 1) {
+        sh.cpre[kBins] = cs;
+        sh.wpre[kBins] = ws;
+    }
+    if (threadIdx.x == 0)
+        sh.n = sh.passed = 0;
+    __syncthreads();
 
-    // The place of a border: the bin with the first token that has `c` tokens and
-    // `w` of the weights up to and with it; then within the bin.
-    struct Border {
-        double weight;      // up to the token and with it
-        Found f;
-        int bin;
+    // the first bin with c tokens, or w of the weights (`past`: more), up to its end; the last one with any where there is none
+    auto bin_of = [&](uint32_t c, double w, bool past) {
+        int b = first_of(kBins, [&](int i) {
+            const double x = sh.wpre[i + 1];
+            return sh.cpre[i + 1] >= c && (past ? x > w : x >= w);
+        });
+        // roundings of the sums may end at a bin without tokens: the next one with any, or the last
+        if (sh.cpre[b + 1] == sh.cpre[b]) {
+            const uint32_t next = min(sh.cpre[b] + 1, all);
+            b = first_of(kBins, [&](int i) { return sh.cpre[i + 1] >= next; });
+        }
+        return b;
     };
-    // where the kept tokens end; nothing is looked for past it
-    Border cap{total, {}, kBins};
+
+    // Which bins hold a border, and between what the kept weight lies.
+    const int32_t k = a.top_k ? a.top_k[row] : a.top_k_all;
+    const float p = a.top_p ? a.top_p[row] : a.top_p_all;
+    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all, least = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
+    const bool by_k = k > 0 && (uint32_t)k < all, by_p = p < 1.0f, by_least = least > 0.0f && !s.alone && !s.flat;
+    constexpr double kLess = 1.0 - 0x1p-45, kMore = 1.0 + 0x1p-45;     // roundings of the sums
+    const float u = a.u[row] > 0.0f ? a.u[row] : 0.0f;
+    // below the kept weight whatever u
+    auto target = [&](double kept) { return fmin((double)u * kept, kept * (1.0 - 0x1p-52)); };
+    if (threadIdx.x < 64) {
+        Ranges &r = sh.r;
+        int n = 0;
+        auto want = [&](int lo, int hi) {
+            // in the order of the bins, joined where they meet
+            int i = 0;
+            while (i < n && r.hi[i] < lo)
+                ++i;
+            int j = i;
+            while (j < n && r.lo[j] <= hi) {
+                lo = min(lo, r.lo[j]);
+                hi = max(hi, r.hi[j]);
+                ++j;
+            }
+            if (j == i) {
+                for (int q = n; q > i; --q)
+                    r.lo[q] = r.lo[q - 1], r.hi[q] = r.hi[q - 1];
+                ++n;
+            } else {
+                for (int q = j; q < n; ++q)
+                    r.lo[i + 1 + q - j] = r.lo[q], r.hi[i + 1 + q - j] = r.hi[q];
+                n -= j - i - 1;
+            }
+            r.lo[i] = lo;
+            r.hi[i] = hi;
+        };
+        double wlo = total * kLess, whi = total * kMore;
+        int last_bin = kBins - 1, least_lo = kBins;
+        auto kept_within = [&](int lo, int hi) {
+            want(lo, hi);
+            last_bin = hi;
+            wlo = fmin(wlo, sh.wpre[lo] * kLess);
+            whi = fmin(whi, sh.wpre[hi + 1] * kMore);
+        };
+        if (by_k) {
+            const int b = bin_of((uint32_t)k, 0.0, false);
+            kept_within(b, b);
+        }
+        if (by_p) {
+            const int lo = min(bin_of(1, p > 0.0f ? (double)p * wlo : 0.0, false), last_bin);
+            kept_within(lo, min(bin_of(1, p > 0.0f ? (double)p * whi : 0.0, false), last_bin));
+        }
+        if (by_least) {
+            // exp((l - top) / T) >= min_p from top + T ln(min_p) on, give or take the roundings
+            const double z = s.t * log((double)least), off = 1e-13 * (fabs((double)top) + fabs(z) + s.t);
+            const double lo = (double)s.top_bin - floor(ldexp((double)top + z + off, s.shift));
+            const double hi = (double)s.top_bin - floor(ldexp((double)top + z - off, s.shift));
+            const int first = (int)fmax(0.0, fmin(lo, (double)kBins));
+            if (first <= last_bin) {
+                least_lo = first;
+                kept_within(first, min((int)fmin(hi, (double)kBins - 1), last_bin));
+                sh.least_hi = last_bin;
+            }
+        }
+        const int lo = min(bin_of(1, target(wlo), true), last_bin), hi = min(bin_of(1, target(whi), true), last_bin);
+        want(min(lo, hi), hi);
+        uint32_t listed = 0;
+        for (int i = 0; i < n; ++i) {
+            listed += sh.cpre[r.hi[i] + 1] - sh.cpre[r.lo[i]];
+            d.span(r.lo[i], r.hi[i], r.from[i], r.to[i]);
+        }
+        r.n = n;
+        // each range costs a comparison with every logit, a token read in vain some more: one range where few lie between
+        r.read = n;
+        const uint32_t between = sh.cpre[r.hi[n - 1] + 1] - sh.cpre[r.lo[0]] - listed;
+        if (n > 1 && between <= (uint32_t)a.vocab / 64) {
+            r.read = 1;
+            r.from[0] = r.from[n - 1];
+        }
+        sh.listed = listed;
+        sh.least_lo = least_lo;
+    }
+    __syncthreads();
+    const Ranges &r = sh.r;
+    auto heavy = [&](float x) { return exp(((double)x - (double)top) / s.t) >= (double)least; };
+    const uint32_t listed = sh.listed;
+    const int least_lo = sh.least_lo;
+    bool gathered = listed <= kList;
+    if (gathered) {
+        switch (r.read) {
+        case 1: d.template pick<1>(r.from, r.to); break;
+        case 2: d.template pick<2>(r.from, r.to); break;
+        case 3: d.template pick<3>(r.from, r.to); break;
+        default: d.template pick<4>(r.from, r.to); break;
+        }
+        __syncthreads();
+        const uint32_t n = sh.n;
+        gathered = n <= (uint32_t)Draw<TH, T>::kPicked;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            sh.n = 0;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; gathered && i < n; i += TH) {
+            const uint32_t at = d.picked()[i];
+            const float x = one_of(d.row, (int)at), b = s.bin(x);
+            bool within = false;
+            for (int j = 0; j < r.n; ++j)
+                within |= b >= (float)r.lo[j] && b <= (float)r.hi[j];
+            if (!within)
+                continue;
+            if (b >= (float)least_lo && heavy(x))
+                atomicAdd(&sh.passed, 1u);
+            d.list[min(atomicAdd(&sh.n, 1u), (uint32_t)kList - 1)] = (uint64_t)~key_of(x) << 32 | at;
+        }
+        __syncthreads();
+        if (gathered)
+            d.order((int)listed, &r, 0, 0);
+    }
+    if (!gathered && least_lo < kBins) {
+        float lo, hi;
+        d.span(least_lo, sh.least_hi, lo, hi);
+        d.each(lo, hi, [&](int, float x) {
+            if (s.bin(x) <= (float)sh.least_hi && heavy(x))
+                atomicAdd(&sh.passed, 1u);
+        });
+        __syncthreads();
+    }
+    // what is left is one wave's work, as long as the list has what is looked for
+    if (gathered && threadIdx.x >= 64)
+        return;
+
+    // Where the kept tokens end; nothing is looked for past it.
+    Border cap{total, kBins, {0, 0}};
     auto border = [&](uint32_t c, double w, bool past) -> Border {
-        __syncthreads();
-        uint32_t cs = cbefore;
-        double ws = wbefore;
-        int mine = -1, last = -1;
-        uint32_t cmine = 0;
-        double wmine = 0;
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-            if (count[i]) {
-                const bool reached = cs + count[i] >= c && (past ? ws + weight[i] > w : ws + weight[i] >= w);
-                if (reached && mine < 0)
-                    mine = b0 + i, cmine = cs, wmine = ws;
-                last = b0 + i;
-            }
-            cs += count[i];
-            ws += weight[i];
+        int b = bin_of(c, w, past);
+        if (b > cap.bin) {
+            if (!past)
+                return cap;
+            b = cap.bin;
         }
-        // the first such bin; next to the end of all weights roundings may leave none, then the last one
-        int hit = mine >= 0 ? mine : 0x7FFFFFFF;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1)
-            hit = min(hit, __shfl_xor(hit, o)), last = max(last, __shfl_xor(last, o));
-        if ((threadIdx.x & 63) == 0)
-            sh.part_c[threadIdx.x >> 6] = (uint32_t)hit, sh.part_u[threadIdx.x >> 6] = (unsigned long long)(last + 1);
-        __syncthreads();
-        for (int i = 0; i < kThreads / 64; ++i)
-            hit = min(hit, (int)sh.part_c[i]), last = max(last, (int)sh.part_u[i] - 1);
-        const bool none = hit == 0x7FFFFFFF;
-        if (none)
-            hit = last;
-        if (hit > cap.bin)
-            return cap;
-        if (hit / per == (int)threadIdx.x) {
-            if (hit != mine) {
-                cmine = cbefore, wmine = wbefore;
-                for (int i = 0; i < hit % per; ++i)
-                    cmine += count[i], wmine += weight[i];
-            }
-            sh.n = cmine;
-            sh.before = wmine;
-        }
-        __syncthreads();
-        const uint32_t before = sh.n;
-        const double wb = sh.before, edge = s.edge(hit, t);
-        __syncthreads();
-        // whole units of the bin's weight that the token has to reach
+        const uint32_t before = sh.cpre[b], n = sh.cpre[b + 1] - before;
+        if (c == before + n && !(w > 0.0) && !past)
+            return {sh.wpre[b + 1], b, {0, ~0ull}};      // the bin's end, of whatever tokens
+        const double wb = sh.wpre[b], edge = s.edge_weight(b);
+        // whole units of the bin's weight that the token has to reach, of those that the limits keep
         double units = (w - wb) / edge * kOne;
         units = past ? floor(units) + 1.0 : ceil(units);
         Query q;
         q.count = c > before ? c - before : 0;
-        // of what is there, and of what the limits keep
-        q.weight = units > 0 ? min((uint64_t)units, hit == cap.bin ? cap.f.weight : sh.sums[hit]) : 0;
+        q.weight = units > 0 ? (uint64_t)fmin(units, 0x1p62) : 0;
+        if (b == cap.bin && q.weight > cap.f.weight)
+            q.weight = cap.f.weight;
         if (q.count == 0 && q.weight == 0)
             q.count = 1;
-        const Found f = d.find(hit, sh.counts[hit], q);
-        return {wb + (double)f.weight * (1.0 / kOne) * edge, f, hit};
-    };
-
-    auto keep = [&](const Border &e) {
-        if (e.bin < cap.bin || (e.bin == cap.bin && e.f.weight < cap.f.weight))
-            cap = e;
-    };
-    const int32_t k = a.top_k ? a.top_k[row] : a.top_k_all;
-    if (k > 0 && (uint32_t)k < all)
-        keep(border((uint32_t)k, -1.0, false));
-    const float p = a.top_p ? a.top_p[row] : a.top_p_all;
-    if (p < 1.0f)
-        keep(border(1, p > 0.0f ? (double)p * cap.weight : 0.0, false));
-    const float least = a.min_p ? a.min_p[row] : a.min_p_all;
-    if (least > 0.0f) {
-        // how many tokens weigh at least min_p (one at most: the first token stays)
-        const double floor_p = fmin((double)least, 1.0);
-        uint32_t mine = 0, n;
-        for (int at = threadIdx.x * 8; at < a.vocab; at += kThreads * 8) {
-            float l[8];
-            load8(d.row + at, min(a.vocab - at, 8), l);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                double below;
-                if (s.bin(l[i], below) < kBins)
-                    mine += s.drawn_max || s.flat || exp(((double)l[i] - (double)top) / t) >= floor_p ? 1 : 0;
-            }
+        Found f;
+        int at = 0;              // of the bin's tokens in the list
+        bool within = false;
+        for (int i = 0; i < r.n; ++i) {
+            at += (int)(sh.cpre[min(max(b, r.lo[i]), r.hi[i] + 1)] - sh.cpre[r.lo[i]]);
+            within |= b >= r.lo[i] && b <= r.hi[i];
         }
-        scan(mine, sh.part_c, n);
-        if (n < all)
-            keep(border(n, -1.0, false));
+        if (gathered && within)
+            f = d.among(at, (int)n, 0, 0, q);
+        else if (!gathered)
+            f = d.search(b, n, q);
+        else
+            f = {d.list[listed - 1], ~0ull};      // not met: the ranges allow for the sums' roundings
+        return {wb + (double)f.weight * (1.0 / kOne) * edge, b, f};
+    };
+    const uint32_t passed = least_lo < kBins ? sh.cpre[least_lo] + sh.passed : all;
+    uint64_t entry = 0;
+    double kept = 0;
+#pragma unroll 1
+    for (int stage = 0; stage < 4; ++stage) {
+        uint32_t c = 1;
+        double w = 0.0;
+        if (stage == 0) {
+            if (!by_k)
+                continue;
+            c = (uint32_t)k;
+        } else if (stage == 1) {
+            if (!by_p)
+                continue;
+            w = p > 0.0f ? (double)p * cap.weight : 0.0;
+        } else if (stage == 2) {
+            if (passed >= all)
+                continue;
+            c = passed;
+        } else {
+            kept = cap.weight;
+            w = target(kept);
+        }
+        const Border e = border(c, w, stage == 3);
+        if (stage == 3)
+            entry = e.f.entry;
+        else if (e.bin < cap.bin || (e.bin == cap.bin && e.f.weight < cap.f.weight))
+            cap = e;
     }
-    // below the kept sum whatever u
-    const double kept = cap.weight;
-    const float u = a.u[row];
-    double target = u > 0.0f ? (double)u * kept : 0.0;
-    if (!(target < kept))
-        target = kept * (1.0 - 0x1p-52);
-    const Found f = border(1, target, true).f;
     if (threadIdx.x == 0) {
-        a.tokens[row] = f.token;
+        a.tokens[row] = (int32_t)entry;
         if (a.logprobs) {
-            const double z = s.drawn_max || s.flat ? 0.0 : ((double)logit_of(f.key) - (double)top) / t;
+            const double z = s.alone || s.flat ? 0.0 : ((double)logit_of(~(uint32_t)(entry >> 32)) - (double)top) / s.t;
             a.logprobs[row] = (float)(z - log(kept));
         }
     }
 }
 
-// Logits a workgroup takes: as many as leave two workgroups a CU, at most 65536.
+// Groups of eight logits a thread of sample_bins: as many as leave two
+// workgroups a CU, up to what fits the registers of 32 waves a CU.
 int groups(int64_t m, int64_t vocab)
 {
-    int g = 8;
-    while (g > 1 && m * ((vocab + g * 8 * kThreads - 1) / (g * 8 * kThreads)) < 512)
+    int g = 4;
+    while (g > 1 && m * ((vocab + g * 8 * kBinThreads - 1) / (g * 8 * kBinThreads)) < 512)
         g /= 2;
     return g;
+}
+
+int parts_of(int64_t m, int64_t vocab)
+{
+    const int64_t part = (int64_t)groups(m, vocab) * 8 * kBinThreads;
+    return (int)((vocab + part - 1) / part);
 }
 
 template <typename T>
 void start(const SampleArgs &a, Part *parts, hipStream_t s)
 {
-    const int g = groups(a.m, a.vocab);
-    const int splits = (a.vocab + g * 8 * kThreads - 1) / (g * 8 * kThreads);
+    const int splits = parts_of(a.m, a.vocab);
     const dim3 grid((unsigned)(a.m * splits));
-    switch (g) {
-    case 8: sample_bins<8, T><<<grid, kThreads, 0, s>>>(a, parts, splits); break;
-    case 4: sample_bins<4, T><<<grid, kThreads, 0, s>>>(a, parts, splits); break;
-    case 2: sample_bins<2, T><<<grid, kThreads, 0, s>>>(a, parts, splits); break;
-    default: sample_bins<1, T><<<grid, kThreads, 0, s>>>(a, parts, splits); break;
+    switch (groups(a.m, a.vocab)) {
+    case 4: sample_bins<4, T><<<grid, kBinThreads, 0, s>>>(a, parts, splits); break;
+    case 2: sample_bins<2, T><<<grid, kBinThreads, 0, s>>>(a, parts, splits); break;
+    default: sample_bins<1, T><<<grid, kBinThreads, 0, s>>>(a, parts, splits); break;
     }
-    sample_draw<T><<<(unsigned)a.m, kThreads, 0, s>>>(a, parts, splits);
+    // up to a row a CU the wider form is faster; of more rows one is at its borders while another is read
+    if (a.m <= 256)
+        sample_draw<1024, T><<<(unsigned)a.m, 1024, 0, s>>>(a, parts, splits);
+    else
+        sample_draw<512, T><<<(unsigned)a.m, 512, 0, s>>>(a, parts, splits);
 }
 
 }  // namespace
 
 size_t sample_workspace_bytes(int64_t m, int64_t vocab)
 {
-    const int64_t chunk = (int64_t)groups(m, vocab) * 8 * kThreads;
-    return (size_t)(m * ((vocab + chunk - 1) / chunk)) * sizeof(Part);
+    return (size_t)(m * parts_of(m, vocab)) * sizeof(Part);
 }
 
 hipError_t launch_sample(const SampleArgs &a, void *workspace, hipStream_t s)
