@@ -10,12 +10,15 @@ namespace bd {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// The signs enter the matrix unit as bytes b of 0 and 1 (one shift and one mask
-// for four of them): sum q sign = 2 sum q b - sum q.  Dword i (0..7) of the 32
-// signs in `w` holds the bits i, i + 8, i + 16, i + 24.
-__device__ __forceinline__ uint32_t sign_bytes(uint32_t w, int i) { return (w >> i) & 0x01010101u; }
+// The signs enter the matrix unit as bytes of 0 and 2 (one shift and one mask for
+// four of them): sum q sign = sum q (2 b) - sum q.  Dword i (0..7) of the 32 signs
+// in `w` holds twice the bits i, i + 8, i + 16, i + 24.
+__device__ __forceinline__ uint32_t twice_sign_bytes(uint32_t w, int i)
+{
+    return (i == 0 ? w << 1 : w >> (i - 1)) & 0x02020202u;
+}
 
-// The 32 bytes X0..X7 put into the order of sign_bytes: dword i becomes the
+// The 32 bytes X0..X7 put into the order of twice_sign_bytes: dword i becomes the
 // bytes i, i + 8, i + 16, i + 24 (two transposes of 4 x 4 bytes).
 __device__ __forceinline__ void to_sign_order(u32x4 &lo, u32x4 &hi)
 {
@@ -39,6 +42,20 @@ __device__ __forceinline__ i32x4 mfma16(u32x4 a, u32x4 b, i32x4 c)
 {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
+
+// Bytes that 64 lanes load (16 or 4 each) straight into LDS, one lane after another.
+template <int CACHE = 0>
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint8_t *to, uint32_t lane_offset, uint32_t offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, lane_offset, offset, 0, CACHE);
+}
+__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, uint8_t *to, uint32_t lane_offset, uint32_t offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 4, lane_offset, offset, 0, 0);
+}
+
+// lgkmcnt(0) alone.
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
 // y = s (c A + alpha B): the sums are exact, and 64 bits here cost nothing
 // beside them, so what is left is the rounding to the output's type.

@@ -39,16 +39,6 @@ __device__ __forceinline__ i32x16 mfma32(u32x4 a, u32x4 b, i32x16 c)
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// Bytes 64 lanes load (16 or 4 each) straight into LDS, one lane after another.
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint8_t *to, uint32_t lane_offset, uint32_t offset)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, lane_offset, offset, 0, 0);
-}
-__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, uint8_t *to, uint32_t lane_offset, uint32_t offset)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 4, lane_offset, offset, 0, 0);
-}
-
 // Four signs (bits at .. at + 3 of w) as bytes of +1 and -1: the bits spread to
 // a byte each by a product, which then picks 0xFF or 0x01.
 __device__ __forceinline__ uint32_t signed_bytes(uint32_t w, int at)
