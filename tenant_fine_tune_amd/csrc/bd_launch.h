@@ -52,9 +52,11 @@ hipError_t launch_gemm(const uint16_t *x, int64_t m, const uint16_t *w_base, con
 // Grouped: bucketing writes this table into the workspace, then the grouped
 // GEMM walks it.  Layout (int32 words): [0] total tiles, [1..3] pad,
 // then perm[m], tile_v[max_tiles], tile_row0[max_tiles], tile_rows[max_tiles].
-int64_t grouped_max_tiles(int64_t m, int32_t n_variants);
-size_t grouped_workspace_bytes(int64_t m, int32_t n_variants);
-hipError_t launch_bucket_tokens(const int32_t *ids, int64_t m, int32_t n_variants, int32_t *table, hipStream_t s);
+// Tiles are tile_m tokens high.
+int64_t grouped_max_tiles(int64_t m, int32_t n_variants, int32_t tile_m = kGemmBM);
+size_t grouped_workspace_bytes(int64_t m, int32_t n_variants, int32_t tile_m = kGemmBM);
+hipError_t launch_bucket_tokens(const int32_t *ids, int64_t m, int32_t n_variants, int32_t tile_m, int32_t *table,
+                                hipStream_t s);
 hipError_t launch_grouped(const uint16_t *x, int64_t m, const int32_t *ids, int32_t n_variants,
                           const uint16_t *w_base, const uint8_t *signs, const float *alpha,
                           bool per_matrix, int64_t d_out, int64_t d_in, uint16_t *y,

@@ -663,7 +663,7 @@ constexpr int kBucketThreads = 1024;
 constexpr int kMaxVariants = 4096;
 
 __global__ __launch_bounds__(kBucketThreads) void bucket_tokens(const int32_t *__restrict__ ids, int64_t M,
-                                                                int32_t V, int64_t max_tiles,
+                                                                int32_t V, int32_t tile_m, int64_t max_tiles,
                                                                 int32_t *__restrict__ table)
 {
     __shared__ int32_t cnt[kMaxVariants + 1];
@@ -684,7 +684,7 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_tokens(const int32_t *_
             seg[i] = s;
             tstart[i] = ts;
             s += cnt[i];
-            ts += (cnt[i] + BM - 1) / BM;
+            ts += (cnt[i] + tile_m - 1) / tile_m;
         }
         seg[nb] = s;
         tstart[nb] = ts;
@@ -714,10 +714,10 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_tokens(const int32_t *_
             else
                 hi = mid - 1;
         }
-        const int32_t r0 = seg[lo] + (ti - tstart[lo]) * BM;
+        const int32_t r0 = seg[lo] + (ti - tstart[lo]) * tile_m;
         tile_v[ti] = lo;
         tile_row0[ti] = r0;
-        tile_rows[ti] = min(BM, seg[lo + 1] - r0);
+        tile_rows[ti] = min(tile_m, seg[lo + 1] - r0);
     }
 }
 
@@ -886,14 +886,14 @@ hipError_t launch_gemm(const uint16_t *x, int64_t m, const uint16_t *w_base, con
                                 tiles - p.tail, p.tail, p.tail_splits, part, s);
 }
 
-int64_t grouped_max_tiles(int64_t m, int32_t n_variants)
+int64_t grouped_max_tiles(int64_t m, int32_t n_variants, int32_t tile_m)
 {
-    return (m + BM - 1) / BM + (int64_t)n_variants + 1;
+    return (m + tile_m - 1) / tile_m + (int64_t)n_variants + 1;
 }
 
-size_t grouped_workspace_bytes(int64_t m, int32_t n_variants)
+size_t grouped_workspace_bytes(int64_t m, int32_t n_variants, int32_t tile_m)
 {
-    return sizeof(int32_t) * (size_t)(4 + m + 3 * grouped_max_tiles(m, n_variants));
+    return sizeof(int32_t) * (size_t)(4 + m + 3 * grouped_max_tiles(m, n_variants, tile_m));
 }
 
 // ---------------------------------------------------------------------------
@@ -939,10 +939,11 @@ hipError_t grouped_scratch(int32_t **table)
     return hipSuccess;
 }
 
-hipError_t launch_bucket_tokens(const int32_t *ids, int64_t m, int32_t n_variants, int32_t *table, hipStream_t s)
+hipError_t launch_bucket_tokens(const int32_t *ids, int64_t m, int32_t n_variants, int32_t tile_m, int32_t *table,
+                                hipStream_t s)
 {
-    hipLaunchKernelGGL(bucket_tokens, dim3(1), dim3(kBucketThreads), 0, s, ids, m, n_variants,
-                       grouped_max_tiles(m, n_variants), table);
+    hipLaunchKernelGGL(bucket_tokens, dim3(1), dim3(kBucketThreads), 0, s, ids, m, n_variants, tile_m,
+                       grouped_max_tiles(m, n_variants, tile_m), table);
     return hipGetLastError();
 }
 
@@ -952,7 +953,7 @@ hipError_t launch_grouped(const uint16_t *x, int64_t m, const int32_t *ids, int3
                           int32_t *workspace, hipStream_t s)
 {
     const int64_t T = grouped_max_tiles(m, n_variants);
-    const hipError_t e = launch_bucket_tokens(ids, m, n_variants, workspace, s);
+    const hipError_t e = launch_bucket_tokens(ids, m, n_variants, BM, workspace, s);
     if (e != hipSuccess)
         return e;
     if (!w8_shape(d_out, d_in))

@@ -638,10 +638,25 @@ hipError_t stream(const Int8Args &a, hipStream_t s)
     return hipGetLastError();
 }
 
+// Whether 65 to 128 tokens of many variants go as two lots of 64: a tile has one
+// variant's tokens, few of its rows, and reads all of the base's for them.
+//   us, 100 tokens              tiles   two lots
+//   8192 x 8192, 4 variants        63         74
+//               14                158        128
+//               30 (of 64)        262        177
+//   1024 x 8192, 14                36         52   (too few workgroups)
+//   28672 x 8192, 14              429        469
+bool twice(const Int8Args &a)
+{
+    const int64_t blocks = (a.m + 63) / 64;
+    return a.ids && blocks == 2 && a.n_variants >= 12 && (a.d_out + 63) / 64 * blocks * mid_splits<4>(a.m, a.d_out, a.d_in) >= 256;
+}
+
 }  // namespace
 
 // Up to 16 tokens the waves of a workgroup share the columns, up to 64 they share
-// the tokens; from there on the tiles are used.
+// the tokens; from there on the tiles are used.  8192 x 8192, one delta: 16 tokens
+// 21 us, 24 tokens 23, 64 tokens 31, 65 tokens 33.
 constexpr int64_t kMidFrom = 17, kTilesFrom = 65;
 
 size_t linear_int8_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
@@ -650,13 +665,13 @@ size_t linear_int8_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out,
         return 0;
     const size_t mid = m <= 32 ? mid_workspace<2>(m, n_variants > 0, d_out, d_in)
                                : mid_workspace<4>(m, n_variants > 0, d_out, d_in);
-    const size_t tiles = m < kTilesFrom ? 0 : int8_tiles_workspace_bytes(m, n_variants);
+    const size_t tiles = m < kTilesFrom ? 0 : int8_tiles_workspace_bytes(m, n_variants, d_out, d_in);
     return mid > tiles ? mid : tiles;
 }
 
 hipError_t launch_linear_int8(const Int8Args &a, void *workspace, hipStream_t s)
 {
-    if (a.m >= kTilesFrom && int8_tiles_take(a))
+    if (a.m >= kTilesFrom && !twice(a) && int8_tiles_take(a))
         return launch_int8_tiles(a, workspace, s);
     if (a.m < kMidFrom)
         return a.ids ? stream<8, true, true>(a, s) : a.signs ? stream<8, true, false>(a, s) : stream<8, false, false>(a, s);

@@ -2,14 +2,18 @@
 // (bitdelta_linear_int8; the formula stands in linear_int8.hip).  Bound by the
 // matrix units.
 //
-// A workgroup of eight waves forms a tile of BM tokens x BN channels, 128
-// columns a step.  The tokens' and the base's rows of a step are copied into
-// LDS directly, NBUF - 1 steps ahead, and every wave reads its operands from
-// there.  With a delta each tile has two sets of sums: the tokens' operands of a
-// step meet the base's bytes and the signs', which the waves spread from bits
-// to bytes of +-1 in registers (16 bytes of signs a channel and step come
-// through LDS too).  Sums of whole numbers are exact, so the two products need
-// no common scale, and nothing of W_eff is ever formed.
+// A workgroup of four waves forms a tile of BM (64 or 128) tokens x 128 channels,
+// 128 columns a step.  The tokens' and the base's rows of a step are copied into
+// LDS directly, a step ahead, and every wave reads its operands from there: its
+// 32 channels and all the tokens.  With a delta each tile has two sets of sums: the
+// tokens' operands of a step meet the base's bytes and the signs', which the wave
+// spreads from bits to bytes of +-1 in registers, each once (16 bytes of signs a
+// channel and step come through LDS too).  Sums of whole numbers are exact, so the
+// two products need no common scale, nothing of W_eff is ever formed, and the
+// columns may be split over workgroups where the tiles are few.
+// Two or three workgroups a compute unit hide each other's waits.  2048 tokens
+// through 8192 x 8192 with one delta: four waves of 32 channels 262 us; four of 64
+// tokens x 64 channels 285; eight in a tile of 256 x 128 alone on its unit 300.
 //
 // In LDS the 16-byte chunk c of row r stands at c ^ ((r >> 1) & 7), so that the
 // reads of 32 rows spread over the banks.  One barrier a step.
@@ -23,7 +27,8 @@ namespace bd {
 namespace {
 
 constexpr int kStep = 128;    // columns (bytes) a step
-constexpr int kWaves = 8;
+constexpr int kBN = 128;      // channels a tile
+constexpr int kWaves = 4;
 constexpr int kXcds = 8;
 
 __device__ __forceinline__ int64_t xcd_remap(int64_t b, int64_t nb)
@@ -47,41 +52,61 @@ __device__ __forceinline__ uint32_t signed_bytes(uint32_t w, int at)
     return __builtin_amdgcn_perm(0u, 0x000001FFu, spread);
 }
 
-// BM x BN tile by WM x WN waves; GATHER: tokens ordered by variant, the table of
-// bucket_tokens.
-template <int BM, int BN, int WM, int WN, int NBUF, bool DELTA, bool GATHER>
-__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_fast, const int32_t *__restrict__ table)
+// The output tile of a workgroup.  Tiles that meet the same rows of w (or, with
+// n_fast, of the tokens) are neighbours, and so on one die.
+struct Place {
+    int64_t mt, nt;
+    int split;
+};
+__device__ __forceinline__ Place place_of(int64_t at, int64_t m_tiles, int64_t n_tiles, bool n_fast, int splits)
 {
-    static_assert(WM * WN == kWaves && (NBUF == 2 || NBUF == 3), "waves, buffers");
-    constexpr int MB = BM / WM / 32, NB = BN / WN / 32;
-    constexpr int XI = BM / 8 / kWaves, WI = BN / 8 / kWaves, SI = DELTA ? BN / 16 / kWaves : 0;
+    if (n_fast)
+        return {at / n_tiles / splits, at % n_tiles, (int)(at / n_tiles % splits)};
+    return {at % m_tiles, at / m_tiles / splits, (int)(at / m_tiles % splits)};
+}
+
+// Token of row `row` of a tile, or -1.
+template <int BM, bool GATHER>
+__device__ __forceinline__ int32_t token_of(const Int8Args &a, const int32_t *table, int64_t mt, int row)
+{
+    if constexpr (GATHER) {
+        const int64_t entries = (a.m + BM - 1) / BM + a.n_variants + 1;    // of grouped_max_tiles
+        const int32_t *perm = table + 4, *row0 = perm + a.m + entries, *rows = row0 + entries;
+        return row < rows[mt] ? perm[row0[mt] + row] : -1;
+    }
+    return mt * BM + row < a.m ? (int32_t)(mt * BM + row) : -1;
+}
+
+// One tile, one of `splits` parts of the columns (with more than one the sums go to
+// `partial`); GATHER: tokens ordered by variant, the table of bucket_tokens.
+template <int BM, bool DELTA, bool GATHER>
+__global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, BM == 64 ? 3 : 2)))
+void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int splits, const int32_t *__restrict__ table,
+                i32x4 *__restrict__ partial)
+{
+    constexpr int MB = BM / 32;                // blocks of 32 tokens, by the wave's 32 channels
+    constexpr int XI = BM / 8 / kWaves, WI = kBN / 8 / kWaves, SI = DELTA ? kBN / 16 / kWaves : 0;
     constexpr int kCopies = XI + WI + SI;      // of a wave and step
-    __shared__ __attribute__((aligned(16))) uint8_t xs[NBUF][BM * kStep], ws[NBUF][BN * kStep];
-    __shared__ __attribute__((aligned(16))) uint8_t ss[DELTA ? NBUF : 1][DELTA ? BN * 16 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t xs[2][BM * kStep], ws[2][kBN * kStep];
+    __shared__ __attribute__((aligned(16))) uint8_t ss[DELTA ? 2 : 1][DELTA ? kBN * 16 : 16];
     __shared__ int32_t rows_s[BM];
     __shared__ float scale_s[BM];
 
     const int lane = threadIdx.x & 63, hi = lane >> 5, low = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
     const int64_t K = a.d_in, N = a.d_out, G = K >> 3;
-    const int64_t tile = xcd_remap(blockIdx.x, gridDim.x);
-    const int64_t mt = n_fast ? tile / n_fast : tile % m_tiles, nt = n_fast ? tile % n_fast : tile / m_tiles;
-    const int64_t n0 = nt * BN;
+    const int64_t at = xcd_remap(blockIdx.x, gridDim.x);
+    const auto [mt, nt, split] = place_of(at, m_tiles, n_tiles, n_fast, splits);
+    const int64_t n0 = nt * kBN;
 
     int variant = 0;
     if constexpr (GATHER) {
         if (mt >= table[0])
             return;
-        const int32_t *perm = table + 4, *tile_v = perm + a.m, *row0 = tile_v + m_tiles, *rows = row0 + m_tiles;
-        variant = tile_v[mt];
-        for (int i = threadIdx.x; i < BM; i += kWaves * 64)
-            rows_s[i] = i < rows[mt] ? perm[row0[mt] + i] : -1;
-    } else {
-        for (int i = threadIdx.x; i < BM; i += kWaves * 64)
-            rows_s[i] = mt * BM + i < a.m ? (int32_t)(mt * BM + i) : -1;
+        variant = (table + 4 + a.m)[mt];
     }
+    for (int i = threadIdx.x; i < BM; i += kWaves * 64)
+        rows_s[i] = token_of<BM, GATHER>(a, table, mt, i);
     __syncthreads();
     const bool known = variant < a.n_variants || !DELTA;
     for (int i = threadIdx.x; i < BM; i += kWaves * 64)
@@ -114,11 +139,12 @@ void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_fast, const int32_t *__re
         const int row = (wave * SI + i) * 16 + (lane >> 2);
         soff[i] = n0 + row < N ? (uint32_t)((n0 + row) * G + (lane & 3) * 4) : kInvalidOffset;
     }
-    const int T = (int)((K + kStep - 1) / kStep);
-    const int last = (int)(K - (int64_t)(T - 1) * kStep);     // columns of the last step
+    const int steps = (int)((K + kStep - 1) / kStep), begin = (int)((int64_t)steps * split / splits);
+    const int T = (int)((int64_t)steps * (split + 1) / splits) - begin;
+    const int last = (int)(K - (int64_t)(steps - 1) * kStep);     // columns of the last step
     auto copy = [&](int t, int buf) {
-        const uint32_t k = (uint32_t)t * kStep;
-        const int have = t == T - 1 ? last : kStep;
+        const uint32_t k = (uint32_t)(begin + t) * kStep;
+        const int have = begin + t == steps - 1 ? last : kStep;
 #pragma unroll
         for (int i = 0; i < XI; ++i)
             copy16(rx, xs[buf] + (wave * XI + i) * 1024, xk[i] < have ? xoff[i] : kInvalidOffset, k);
@@ -131,145 +157,257 @@ void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_fast, const int32_t *__re
     };
     const int sw = (low >> 1) & 7;
     auto read_x = [&](u32x4 (&f)[MB], int buf, int kb) {
-        const uint8_t *p = xs[buf] + (wm * MB * 32 + low) * kStep + (((kb * 2 + hi) ^ sw) * 16);
+        const uint8_t *p = xs[buf] + low * kStep + (((kb * 2 + hi) ^ sw) * 16);
 #pragma unroll
         for (int i = 0; i < MB; ++i)
             f[i] = *reinterpret_cast<const u32x4 *>(p + i * 32 * kStep);
     };
-    auto read_w = [&](u32x4 (&f)[NB], int buf, int kb) {
-        const uint8_t *p = ws[buf] + (wn * NB * 32 + low) * kStep + (((kb * 2 + hi) ^ sw) * 16);
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-            f[i] = *reinterpret_cast<const u32x4 *>(p + i * 32 * kStep);
+    auto read_w = [&](u32x4 &f, int buf, int kb) {
+        f = *reinterpret_cast<const u32x4 *>(ws[buf] + (wave * 32 + low) * kStep + (((kb * 2 + hi) ^ sw) * 16));
     };
-    auto read_s = [&](u32x4 (&f)[NB], int buf) {
+    auto read_s = [&](u32x4 &f, int buf) {
         if constexpr (DELTA)
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-                f[i] = *reinterpret_cast<const u32x4 *>(ss[buf] + (wn * NB * 32 + i * 32 + low) * 16);
+            f = *reinterpret_cast<const u32x4 *>(ss[buf] + (wave * 32 + low) * 16);
     };
 
     // Sums in accumulation registers: left in the others, the matrix
     // instructions and the rest contend for one file.
-    i32x16 acc[MB][NB], accd[DELTA ? MB : 1][DELTA ? NB : 1];
+    i32x16 acc[MB], accd[DELTA ? MB : 1];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+    for (int i = 0; i < MB; ++i) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-                acc[i][j][v] = 0;
-            asm volatile("" : "+a"(acc[i][j]));
-            if constexpr (DELTA) {
-                accd[i][j] = acc[i][j];
-                asm volatile("" : "+a"(accd[i][j]));
-            }
+        for (int v = 0; v < 16; ++v)
+            acc[i][v] = 0;
+        asm volatile("" : "+a"(acc[i]));
+        if constexpr (DELTA) {
+            accd[i] = acc[i];
+            asm volatile("" : "+a"(accd[i]));
         }
+    }
 
-#pragma unroll
-    for (int t = 0; t < NBUF; ++t)
-        copy(t < T ? t : T - 1, t);
-    wait_vmcnt<(NBUF - 1) * kCopies>();
+    copy(0, 0);
+    copy(T > 1 ? 1 : 0, 1);
+    wait_vmcnt<kCopies>();
     __syncthreads();
-    u32x4 X[2][MB], W[2][NB], S[2][NB];
+    u32x4 X[2][MB], W[2], S[2];
     read_x(X[0], 0, 0);
     read_w(W[0], 0, 0);
     read_s(S[0], 0);
 
-    auto product = [&](int kb, const u32x4 (&s)[NB]) {
+    auto product = [&](int kb, const u32x4 &s) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+        for (int i = 0; i < MB; ++i)
+            acc[i] = mfma32(X[kb & 1][i], W[kb & 1], acc[i]);
+        if constexpr (DELTA) {
+            u32x4 b;
+            const uint32_t w = s[kb] >> (16 * hi);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                b[c] = signed_bytes(w, 4 * c);
 #pragma unroll
             for (int i = 0; i < MB; ++i)
-                acc[i][j] = mfma32(X[kb & 1][i], W[kb & 1][j], acc[i][j]);
-        if constexpr (DELTA)
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                u32x4 b;
-                const uint32_t w = s[j][kb] >> (16 * hi);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    b[c] = signed_bytes(w, 4 * c);
-#pragma unroll
-                for (int i = 0; i < MB; ++i)
-                    accd[i][j] = mfma32(X[kb & 1][i], b, accd[i][j]);
-            }
+                accd[i] = mfma32(X[kb & 1][i], b, accd[i]);
+        }
     };
     // Step t from buffer cur, whose first operands are in registers.  Before the
     // last of its four products every read of the buffer is done: the barrier, the
-    // copies of step t + NBUF into it, and the first operands of step t + 1, which
+    // copies of step t + 2 into it, and the first operands of step t + 1, which
     // has landed, while that product runs.
-    auto step = [&](int t, auto cur_c, auto odd_c) {
-        constexpr int cur = decltype(cur_c)::value, nxt = (cur + 1) % NBUF, o = decltype(odd_c)::value;
+    auto step = [&](int t, auto cur_c) {
+        constexpr int cur = decltype(cur_c)::value, nxt = 1 - cur;
 #pragma unroll
         for (int kb = 0; kb < 3; ++kb) {
             read_x(X[(kb + 1) & 1], cur, kb + 1);
             read_w(W[(kb + 1) & 1], cur, kb + 1);
-            product(kb, S[o]);
+            product(kb, S[cur]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        wait_vmcnt_lgkm0<(NBUF - 2) * kCopies>();
+        wait_vmcnt_lgkm0<0>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        copy(t + NBUF < T ? t + NBUF : T - 1, cur);
+        copy(t + 2 < T ? t + 2 : T - 1, cur);
         __builtin_amdgcn_sched_barrier(0);
         read_x(X[0], nxt, 0);       // past the last step: copied again, not used
         read_w(W[0], nxt, 0);
-        read_s(S[1 - o], nxt);
-        product(3, S[o]);
+        read_s(S[nxt], nxt);
+        product(3, S[cur]);
         __builtin_amdgcn_sched_barrier(0);
     };
-    constexpr int kTurn = NBUF % 2 ? 2 * NBUF : NBUF;     // steps until buffer and sign registers meet again
-    for (int t = 0; t < T; t += kTurn) {
-        step(t, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
+    for (int t = 0; t < T; t += 2) {
+        step(t, std::integral_constant<int, 0>{});
         if (t + 1 < T)
-            step(t + 1, std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-        if constexpr (kTurn == 6) {
-            if (t + 2 < T)
-                step(t + 2, std::integral_constant<int, 2 % NBUF>{}, std::integral_constant<int, 0>{});
-            if (t + 3 < T)
-                step(t + 3, std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
-            if (t + 4 < T)
-                step(t + 4, std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{});
-            if (t + 5 < T)
-                step(t + 5, std::integral_constant<int, 2 % NBUF>{}, std::integral_constant<int, 1>{});
-        }
+            step(t + 1, std::integral_constant<int, 1>{});
     }
     // copies still on their way must land before the workgroup's LDS is released
     __builtin_amdgcn_s_waitcnt(0);
 
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const int64_t n = n0 + (wn * NB + j) * 32 + low;
-        const float c = n < N ? a.w_scale[n] : 0.0f;
-        float alpha = 0.0f;
-        if (DELTA && known && n < N)
-            alpha = a.alpha[a.per_matrix ? variant : variant * N + n];
+    if (splits > 1) {
+        // in the order of the registers: sums of base and delta, by fours of rows
+        constexpr int kSums = DELTA ? 2 : 1;
+        i32x4 *out = partial + (at * kWaves + wave) * (MB * 4 * kSums * 64) + lane;
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int row = (wm * MB + i) * 32 + 8 * (v >> 2) + 4 * hi + (v & 3);
-                const int32_t token = rows_s[row];
-                if (token < 0 || n >= N)
-                    continue;
-                const float y = known ? combine(scale_s[row], c, acc[i][j][v], alpha, DELTA ? accd[i][j][v] : 0) : 0.0f;
-                if (a.f32)
-                    static_cast<float *>(a.y)[token * N + n] = y;
-                else
-                    static_cast<uint16_t *>(a.y)[token * N + n] = to_bf16(y);
-            }
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < kSums; ++e) {
+                    const i32x16 &from = e ? accd[DELTA ? i : 0] : acc[i];
+                    out[((i * 4 + q) * kSums + e) * 64] = i32x4{from[4 * q], from[4 * q + 1], from[4 * q + 2], from[4 * q + 3]};
+                }
+        return;
+    }
+    const int64_t n = n0 + wave * 32 + low;
+    if (n >= N)
+        return;
+    const float c = a.w_scale[n], alpha = DELTA && known ? a.alpha[a.per_matrix ? variant : variant * N + n] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int row = i * 32 + 8 * (v >> 2) + 4 * hi + (v & 3);
+            const int32_t token = rows_s[row];
+            if (token < 0)
+                continue;
+            const float y = known ? combine(scale_s[row], c, acc[i][v], alpha, DELTA ? accd[i][v] : 0) : 0.0f;
+            if (a.f32)
+                static_cast<float *>(a.y)[token * N + n] = y;
+            else
+                static_cast<uint16_t *>(a.y)[token * N + n] = to_bf16(y);
+        }
+}
+
+// Adds up the parts of int8_tiles: a wave for 32 channels by 8 rows.
+template <int BM, bool DELTA, bool GATHER>
+__global__ __launch_bounds__(kWaves * 64) void int8_tiles_join(Int8Args a, int64_t m_tiles, int64_t n_tiles, bool n_fast,
+                                                       int splits, const int32_t *__restrict__ table,
+                                                       const i32x4 *__restrict__ partial)
+{
+    constexpr int MB = BM / 32, kParts = kWaves * MB * 4, kLane = DELTA ? 128 : 64;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = (int64_t)blockIdx.x * kWaves + wave, tile = id / kParts;
+    if (tile >= m_tiles * n_tiles)
+        return;
+    const int part = (int)(id % kParts), q = part & 3, i = part / 4 % MB, w = part / 4 / MB;
+    // this tile's place among its splits
+    const int64_t mt = n_fast ? tile / n_tiles : tile % m_tiles, nt = n_fast ? tile % n_tiles : tile / m_tiles;
+    if (GATHER && mt >= table[0])
+        return;
+    i32x4 acc = {0, 0, 0, 0}, accd = {0, 0, 0, 0};
+    for (int split = 0; split < splits; ++split) {
+        const int64_t at = n_fast ? (mt * splits + split) * n_tiles + nt : (nt * splits + split) * m_tiles + mt;
+        const i32x4 *in = partial + (at * kParts + part) * kLane + lane;
+        acc += in[0];
+        if constexpr (DELTA)
+            accd += in[64];
+    }
+    const int variant = GATHER ? (table + 4 + a.m)[mt] : 0;
+    const bool known = !DELTA || variant < a.n_variants;
+    const int64_t n = nt * kBN + w * 32 + (lane & 31), N = a.d_out;
+    if (n >= N)
+        return;
+    const float c = a.w_scale[n], alpha = DELTA && known ? a.alpha[a.per_matrix ? variant : variant * N + n] : 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int32_t token = token_of<BM, GATHER>(a, table, mt, i * 32 + 8 * q + 4 * (lane >> 5) + r);
+        if (token < 0)
+            continue;
+        const float y = known ? combine(a.q_scale[token], c, acc[r], alpha, accd[r]) : 0.0f;
+        if (a.f32)
+            static_cast<float *>(a.y)[token * N + n] = y;
+        else
+            static_cast<uint16_t *>(a.y)[token * N + n] = to_bf16(y);
     }
 }
 
-template <int BM, int BN, int WM, int WN, int NBUF, bool DELTA, bool GATHER>
-hipError_t tiles(const Int8Args &a, int64_t m_tiles, const int32_t *table, hipStream_t s)
+size_t table_bytes(int64_t m, int32_t n_variants)
 {
-    const int64_t n_tiles = (a.d_out + BN - 1) / BN;
-    const int64_t n_fast = !GATHER && a.d_out < a.m ? n_tiles : 0;
-    const dim3 grid((unsigned)(m_tiles * n_tiles));
-    int8_tiles<BM, BN, WM, WN, NBUF, DELTA, GATHER><<<grid, kWaves * 64, 0, s>>>(a, m_tiles, n_fast, table);
+    return (grouped_workspace_bytes(m, n_variants, 64) + 15) / 16 * 16;
+}
+
+// Tiles along the tokens; with ids the most there can be (a tile holds tokens of
+// one variant, ids out of range being one more).
+template <int BM>
+int64_t token_tiles(int64_t m, int32_t variants)
+{
+    return variants ? m / BM + (m < variants + 1 ? m : variants + 1) : (m + BM - 1) / BM;
+}
+
+struct Plan {
+    bool tall;      // tiles of 128 tokens, or of 64
+    int splits;
+};
+
+// By what the two tiles take, in us: 512 workgroups of the tall tile fit the card
+// at once and 768 of the other; a step of 128 columns takes them 1.25 and 1.0
+// without a delta, 2.1 and 1.5 with one (8192 x 8192, 512 to 2048 tokens), so that
+// full rounds go 20 % faster through the tall tile and a part of one through the
+// other.  Split columns cost a second launch and the sums' way through memory at
+// 4 TB/s.  With ids, a variant in four is taken to have no tile of its own.
+//   tokens (8192 x 8192, one delta)   64 tall, best split   128 tall, best split
+//     128                              40 (4)                43 (4)
+//     512                              83 (1)                93 (2)
+//    1024                             166 (1)               140 (1)
+//   14 variants, 512                  184 (1)               234 (1)
+//                2048                 379 (1)               375 (1)
+Plan plan_of(int64_t m, int64_t d_out, int64_t d_in, bool delta, int32_t variants)
+{
+    const int64_t steps = (d_in + kStep - 1) / kStep, n_tiles = (d_out + kBN - 1) / kBN;
+    Plan best = {false, 1};
+    double least = 0;
+    for (int tall = 0; tall < 2; ++tall) {
+        const int64_t bm = tall ? 128 : 64, slots = tall ? 512 : 768;
+        const int64_t tiles = ((m + bm - 1) / bm + (variants < m ? variants : m) * 3 / 4) * n_tiles;
+        const double us = tall ? (delta ? 2.1 : 1.25) : (delta ? 1.5 : 1.0);
+        for (int splits = 1; splits <= 16 && (splits == 1 || steps / splits >= 4); splits *= 2) {
+            double cost = (double)((tiles * splits + slots - 1) / slots * ((steps + splits - 1) / splits)) * us;
+            if (splits > 1)
+                cost += 4 + (double)(tiles * splits * bm) * kBN * (delta ? 8 : 4) * 2 / 4e6;
+            if ((!tall && splits == 1) || cost < least) {
+                least = cost;
+                best = {tall != 0, splits};
+            }
+        }
+    }
+    return best;
+}
+
+template <int BM, bool DELTA, bool GATHER>
+hipError_t tiles(const Int8Args &a, int splits, void *workspace, hipStream_t s)
+{
+    const int64_t m_tiles = token_tiles<BM>(a.m, GATHER ? a.n_variants : 0), n_tiles = (a.d_out + kBN - 1) / kBN;
+    int32_t *table = static_cast<int32_t *>(workspace);
+    i32x4 *partial = static_cast<i32x4 *>(workspace);
+    if constexpr (GATHER) {
+        const hipError_t e = launch_bucket_tokens(a.ids, a.m, a.n_variants, BM, table, s);
+        if (e != hipSuccess)
+            return e;
+        partial += table_bytes(a.m, a.n_variants) / 16;
+    }
+    // neighbours share the larger operand
+    const bool n_fast = !GATHER && a.d_out < a.m;
+    const dim3 grid((unsigned)(m_tiles * n_tiles * splits));
+    int8_tiles<BM, DELTA, GATHER><<<grid, kWaves * 64, 0, s>>>(a, m_tiles, n_tiles, n_fast, splits, table, partial);
+    if (splits > 1) {
+        const dim3 joins((unsigned)(m_tiles * n_tiles * (BM / 8)));
+        int8_tiles_join<BM, DELTA, GATHER><<<joins, kWaves * 64, 0, s>>>(a, m_tiles, n_tiles, n_fast, splits, table, partial);
+    }
     return hipGetLastError();
+}
+
+template <bool DELTA, bool GATHER>
+hipError_t planned(const Int8Args &a, void *workspace, hipStream_t s)
+{
+    const Plan p = plan_of(a.m, a.d_out, a.d_in, DELTA, GATHER ? a.n_variants : 0);
+    return p.tall ? tiles<128, DELTA, GATHER>(a, p.splits, workspace, s) : tiles<64, DELTA, GATHER>(a, p.splits, workspace, s);
+}
+
+size_t partial_bytes(int64_t m, int64_t d_out, int64_t d_in, bool delta, int32_t variants)
+{
+    const Plan p = plan_of(m, d_out, d_in, delta, variants);
+    if (p.splits == 1)
+        return 0;
+    const int64_t rows = p.tall ? token_tiles<128>(m, variants) * 128 : token_tiles<64>(m, variants) * 64;
+    return (size_t)(rows * ((d_out + kBN - 1) / kBN) * kBN * p.splits) * (delta ? 8 : 4);
 }
 
 }  // namespace
@@ -277,27 +415,24 @@ hipError_t tiles(const Int8Args &a, int64_t m_tiles, const int32_t *table, hipSt
 bool int8_tiles_take(const Int8Args &a)
 {
     // a launch takes fewer than 2^32 threads
-    const int64_t most = (a.m + 255) / 256 + (a.ids ? a.n_variants + 1 : 0);
-    return a.d_in % 32 == 0 && ((uintptr_t)a.signs & 3) == 0 && most * ((a.d_out + 127) / 128) < (1 << 23);
+    const int64_t most = token_tiles<64>(a.m, a.ids ? a.n_variants : 0);
+    return a.d_in % 32 == 0 && ((uintptr_t)a.signs & 3) == 0 && most * ((a.d_out + kBN - 1) / kBN) < (1 << 23);
 }
 
-size_t int8_tiles_workspace_bytes(int64_t m, int32_t n_variants)
+size_t int8_tiles_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
-    return n_variants > 1 ? grouped_workspace_bytes(m, n_variants) : 0;
+    if (n_variants == 0)
+        return partial_bytes(m, d_out, d_in, false, 0);
+    // whether the call has ids is not known here
+    const size_t one = partial_bytes(m, d_out, d_in, true, 0), many = partial_bytes(m, d_out, d_in, true, n_variants);
+    return table_bytes(m, n_variants) + (one > many ? one : many);
 }
 
 hipError_t launch_int8_tiles(const Int8Args &a, void *workspace, hipStream_t s)
 {
-    const int64_t m_tiles = (a.m + 255) / 256;
     if (!a.signs)
-        return tiles<256, 256, 2, 4, 2, false, false>(a, m_tiles, nullptr, s);
-    if (!a.ids)
-        return tiles<256, 128, 4, 2, 3, true, false>(a, m_tiles, nullptr, s);
-    int32_t *table = static_cast<int32_t *>(workspace);
-    const hipError_t e = launch_bucket_tokens(a.ids, a.m, a.n_variants, table, s);
-    if (e != hipSuccess)
-        return e;
-    return tiles<256, 128, 4, 2, 3, true, true>(a, grouped_max_tiles(a.m, a.n_variants), table, s);
+        return planned<false, false>(a, workspace, s);
+    return a.ids ? planned<true, true>(a, workspace, s) : planned<true, false>(a, workspace, s);
 }
 
 }  // namespace bd
