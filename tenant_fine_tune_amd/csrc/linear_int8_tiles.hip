@@ -337,6 +337,14 @@ struct Plan {
     int splits;
 };
 
+// Sums of all splits' tiles; never more than kMostParts.
+constexpr size_t kMostParts = (size_t)1 << 28;
+size_t part_bytes(bool tall, int64_t m, int64_t d_out, int splits, bool delta, int32_t variants)
+{
+    const int64_t rows = tall ? token_tiles<128>(m, variants) * 128 : token_tiles<64>(m, variants) * 64;
+    return splits == 1 ? 0 : (size_t)(rows * ((d_out + kBN - 1) / kBN) * kBN * splits) * (delta ? 8 : 4);
+}
+
 // By what the two tiles take, in us: 512 workgroups of the tall tile fit the card
 // at once and 768 of the other; a step of 128 columns takes them 1.25 and 1.0
 // without a delta, 2.1 and 1.5 with one (8192 x 8192, 512 to 2048 tokens), so that
@@ -360,8 +368,11 @@ Plan plan_of(int64_t m, int64_t d_out, int64_t d_in, bool delta, int32_t variant
         const double us = tall ? (delta ? 2.1 : 1.25) : (delta ? 1.5 : 1.0);
         for (int splits = 1; splits <= 16 && (splits == 1 || steps / splits >= 4); splits *= 2) {
             double cost = (double)((tiles * splits + slots - 1) / slots * ((steps + splits - 1) / splits)) * us;
-            if (splits > 1)
+            if (splits > 1) {
+                if (part_bytes(tall, m, d_out, splits, delta, variants) > kMostParts)
+                    break;
                 cost += 4 + (double)(tiles * splits * bm) * kBN * (delta ? 8 : 4) * 2 / 4e6;
+            }
             if ((!tall && splits == 1) || cost < least) {
                 least = cost;
                 best = {tall != 0, splits};
@@ -404,10 +415,7 @@ hipError_t planned(const Int8Args &a, void *workspace, hipStream_t s)
 size_t partial_bytes(int64_t m, int64_t d_out, int64_t d_in, bool delta, int32_t variants)
 {
     const Plan p = plan_of(m, d_out, d_in, delta, variants);
-    if (p.splits == 1)
-        return 0;
-    const int64_t rows = p.tall ? token_tiles<128>(m, variants) * 128 : token_tiles<64>(m, variants) * 64;
-    return (size_t)(rows * ((d_out + kBN - 1) / kBN) * kBN * p.splits) * (delta ? 8 : 4);
+    return part_bytes(p.tall, m, d_out, p.splits, delta, variants);
 }
 
 }  // namespace
