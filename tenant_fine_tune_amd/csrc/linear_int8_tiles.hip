@@ -52,6 +52,13 @@ __device__ __forceinline__ uint32_t signed_bytes(uint32_t w, int at)
     return __builtin_amdgcn_perm(0u, 0x000001FFu, spread);
 }
 
+// A call over rows of whole 32 columns: as given, or with the tokens' numbers and
+// the signs in copies that zeros fill up, while w keeps its own stride.  What the
+// tiles then read of w past a row's end meets zeros.
+struct TileArgs : Int8Args {
+    int64_t w_stride;
+};
+
 // The output tile of a workgroup.  Tiles that meet the same rows of w (or, with
 // n_fast, of the tokens) are neighbours, and so on one die.
 struct Place {
@@ -67,7 +74,7 @@ __device__ __forceinline__ Place place_of(int64_t at, int64_t m_tiles, int64_t n
 
 // Token of row `row` of a tile, or -1.
 template <int BM, bool GATHER>
-__device__ __forceinline__ int32_t token_of(const Int8Args &a, const int32_t *table, int64_t mt, int row)
+__device__ __forceinline__ int32_t token_of(const TileArgs &a, const int32_t *table, int64_t mt, int row)
 {
     if constexpr (GATHER) {
         const int64_t entries = (a.m + BM - 1) / BM + a.n_variants + 1;    // of grouped_max_tiles
@@ -81,7 +88,7 @@ __device__ __forceinline__ int32_t token_of(const Int8Args &a, const int32_t *ta
 // `partial`); GATHER: tokens ordered by variant, the table of bucket_tokens.
 template <int BM, bool DELTA, bool GATHER>
 __global__ __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, BM == 64 ? 3 : 2)))
-void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int splits, const int32_t *__restrict__ table,
+void int8_tiles(TileArgs a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int splits, const int32_t *__restrict__ table,
                 i32x4 *__restrict__ partial)
 {
     constexpr int MB = BM / 32;                // blocks of 32 tokens, by the wave's 32 channels
@@ -113,7 +120,7 @@ void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int s
         scale_s[i] = rows_s[i] >= 0 ? a.q_scale[rows_s[i]] : 0.0f;
     const uint8_t *signs = DELTA ? a.signs + (int64_t)(known ? variant : 0) * N * G : nullptr;
 
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.q, a.m * K), rw = make_rsrc(a.w, N * K);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.q, a.m * K), rw = make_rsrc(a.w, N * a.w_stride);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(signs, DELTA ? N * G : 0);
     // copy i of this wave covers 8 rows; lane l writes place l & 7 of row l / 8.
     // Rows that do not exist have an offset out of range (zeros); the step's
@@ -132,7 +139,7 @@ void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int s
     for (int i = 0; i < WI; ++i) {
         const int row = (wave * WI + i) * 8 + (lane >> 3);
         wk[i] = (place ^ ((row >> 1) & 7)) * 16;
-        woff[i] = n0 + row < N ? (uint32_t)((n0 + row) * K + wk[i]) : kInvalidOffset;
+        woff[i] = n0 + row < N ? (uint32_t)((n0 + row) * a.w_stride + wk[i]) : kInvalidOffset;
     }
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
@@ -278,7 +285,7 @@ void int8_tiles(Int8Args a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int s
 
 // Adds up the parts of int8_tiles: a wave for 32 channels by 8 rows.
 template <int BM, bool DELTA, bool GATHER>
-__global__ __launch_bounds__(kWaves * 64) void int8_tiles_join(Int8Args a, int64_t m_tiles, int64_t n_tiles, bool n_fast,
+__global__ __launch_bounds__(kWaves * 64) void int8_tiles_join(TileArgs a, int64_t m_tiles, int64_t n_tiles, bool n_fast,
                                                        int splits, const int32_t *__restrict__ table,
                                                        const i32x4 *__restrict__ partial)
 {
@@ -317,6 +324,29 @@ __global__ __launch_bounds__(kWaves * 64) void int8_tiles_join(Int8Args a, int64
         else
             static_cast<uint16_t *>(a.y)[token * N + n] = to_bf16(y);
     }
+}
+
+// The copies of TileArgs, eight numbers or 32 signs a thread.  G: bytes of a row of
+// signs, any alignment.
+__global__ __launch_bounds__(256) void int8_pad(const uint64_t *__restrict__ q, uint64_t *__restrict__ q_to, uint32_t q_units,
+                                                const uint8_t *__restrict__ signs, uint32_t *__restrict__ signs_to,
+                                                uint32_t sign_units, uint32_t G, uint32_t padded)
+{
+    uint32_t i = blockIdx.x * 256 + threadIdx.x;
+    if (i < q_units) {
+        const uint32_t row = i / padded, at = i % padded;
+        q_to[i] = at < G ? q[row * G + at] : 0;
+        return;
+    }
+    i -= q_units;
+    if (i >= sign_units)
+        return;
+    const uint32_t row = i / (padded / 4), at = i % (padded / 4) * 4;
+    uint32_t w = 0;
+    for (uint32_t b = 0; b < 4; ++b)
+        if (at + b < G)
+            w |= (uint32_t)signs[(uint64_t)row * G + at + b] << (8 * b);
+    signs_to[i] = w;
 }
 
 size_t table_bytes(int64_t m, int32_t n_variants)
@@ -383,7 +413,7 @@ Plan plan_of(int64_t m, int64_t d_out, int64_t d_in, bool delta, int32_t variant
 }
 
 template <int BM, bool DELTA, bool GATHER>
-hipError_t tiles(const Int8Args &a, int splits, void *workspace, hipStream_t s)
+hipError_t tiles(const TileArgs &a, int splits, void *workspace, hipStream_t s)
 {
     const int64_t m_tiles = token_tiles<BM>(a.m, GATHER ? a.n_variants : 0), n_tiles = (a.d_out + kBN - 1) / kBN;
     int32_t *table = static_cast<int32_t *>(workspace);
@@ -406,7 +436,7 @@ hipError_t tiles(const Int8Args &a, int splits, void *workspace, hipStream_t s)
 }
 
 template <bool DELTA, bool GATHER>
-hipError_t planned(const Int8Args &a, void *workspace, hipStream_t s)
+hipError_t planned(const TileArgs &a, void *workspace, hipStream_t s)
 {
     const Plan p = plan_of(a.m, a.d_out, a.d_in, DELTA, GATHER ? a.n_variants : 0);
     return p.tall ? tiles<128, DELTA, GATHER>(a, p.splits, workspace, s) : tiles<64, DELTA, GATHER>(a, p.splits, workspace, s);
@@ -418,16 +448,9 @@ size_t partial_bytes(int64_t m, int64_t d_out, int64_t d_in, bool delta, int32_t
     return part_bytes(p.tall, m, d_out, p.splits, delta, variants);
 }
 
-}  // namespace
+int64_t whole(int64_t d_in) { return (d_in + 31) / 32 * 32; }
 
-bool int8_tiles_take(const Int8Args &a)
-{
-    // a launch takes fewer than 2^32 threads
-    const int64_t most = token_tiles<64>(a.m, a.ids ? a.n_variants : 0);
-    return a.d_in % 32 == 0 && ((uintptr_t)a.signs & 3) == 0 && most * ((a.d_out + kBN - 1) / kBN) < (1 << 23);
-}
-
-size_t int8_tiles_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
+size_t sums_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
     if (n_variants == 0)
         return partial_bytes(m, d_out, d_in, false, 0);
@@ -436,8 +459,51 @@ size_t int8_tiles_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out, 
     return table_bytes(m, n_variants) + (one > many ? one : many);
 }
 
-hipError_t launch_int8_tiles(const Int8Args &a, void *workspace, hipStream_t s)
+// Whether rows that end inside 32 columns are copied for the tiles: the copy of all
+// variants' signs has to be paid for by the tokens (333 tokens of 3 variants through
+// 1000 x 4104: by the kernel for 64 tokens 60 us, copied 33), and stays below 2^28 bytes.
+size_t pad_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
+    return (size_t)(m * whole(d_in) + n_variants * (d_out * (whole(d_in) / 8)) + 31) / 16 * 16;
+}
+bool pads(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
+{
+    return d_in % 32 != 0 && n_variants <= m / 4 && pad_bytes(m, n_variants, d_out, d_in) <= (size_t)1 << 28;
+}
+
+}  // namespace
+
+bool int8_tiles_take(const Int8Args &a)
+{
+    // a launch takes fewer than 2^32 threads
+    const int64_t most = token_tiles<64>(a.m, a.ids ? a.n_variants : 0) * ((a.d_out + kBN - 1) / kBN);
+    const bool rows = a.d_in % 32 == 0 ? ((uintptr_t)a.signs & 3) == 0 : pads(a.m, a.n_variants, a.d_out, a.d_in);
+    return rows && most < (1 << 23);
+}
+
+size_t int8_tiles_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
+{
+    return sums_bytes(m, n_variants, d_out, whole(d_in)) +
+           (pads(m, n_variants, d_out, d_in) ? pad_bytes(m, n_variants, d_out, d_in) : 0);
+}
+
+hipError_t launch_int8_tiles(const Int8Args &args, void *workspace, hipStream_t s)
+{
+    TileArgs a{args, args.d_in};
+    if (a.d_in % 32 != 0) {
+        a.d_in = whole(a.d_in);
+        const int64_t G = a.w_stride / 8, padded = a.d_in / 8;
+        uint8_t *copies = static_cast<uint8_t *>(workspace) + sums_bytes(a.m, a.n_variants, a.d_out, a.d_in);
+        uint64_t *q_to = reinterpret_cast<uint64_t *>(copies);
+        uint32_t *signs_to = reinterpret_cast<uint32_t *>(copies + a.m * a.d_in);
+        const int64_t q_units = a.m * padded, sign_units = a.n_variants * a.d_out * (padded / 4);
+        int8_pad<<<(unsigned)((q_units + sign_units + 255) / 256), 256, 0, s>>>(
+            reinterpret_cast<const uint64_t *>(a.q), q_to, (uint32_t)q_units, a.signs, signs_to, (uint32_t)sign_units, (uint32_t)G,
+            (uint32_t)padded);
+        a.q = reinterpret_cast<const int8_t *>(q_to);
+        if (a.signs)
+            a.signs = reinterpret_cast<const uint8_t *>(signs_to);
+    }
     if (!a.signs)
         return planned<false, false>(a, workspace, s);
     return a.ids ? planned<true, true>(a, workspace, s) : planned<true, false>(a, workspace, s);

@@ -82,8 +82,9 @@ def test_linear_workspace_over_its_range(bd):
                 if m * k >= 2 ** 31 or n * k >= 2 ** 31 or m * n * 2 >= 2 ** 31:
                     continue
                 for v in (0, 1, 14, 4096):
-                    # at most 2^28 of sums, and a table of the tokens by variant: a number a token, three a tile
-                    assert 0 <= ask(m, v, n, k) <= (1 << 28) + 4 * (m + 3 * (m // 64 + v + 2)) + 32
+                    # at most 2^28 of sums and 2^28 of copies, and a table of the tokens by variant: a number
+                    # a token, three a tile
+                    assert 0 <= ask(m, v, n, k) <= (1 << (29 if k % 32 else 28)) + 4 * (m + 3 * (m // 64 + v + 2)) + 32
 
 
 def draw(bd, **kw):
