@@ -153,12 +153,39 @@ struct Part {
     uint64_t bins[kBins];
 };
 
+// What lane's neighbour by a fixed move holds, `none` where there is no such lane
+// or the move does not reach its row of 16.
+constexpr int kUp1 = 0x111, kUp2 = 0x112, kUp4 = 0x114, kUp8 = 0x118;    // within a row
+constexpr int kRow = 0x142, kRows = 0x143;       // from the last lane of the row, of the two rows, before
+constexpr int kWave1 = 0x138;                    // one lane up, over the rows
+template <int MOVE, int ROWS = 15>
+__device__ __forceinline__ uint32_t moved(uint32_t v, uint32_t none)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, MOVE, ROWS, 15, false);
+}
+template <int MOVE, int ROWS = 15>
+__device__ __forceinline__ unsigned long long moved(unsigned long long v, unsigned long long none)
+{
+    return (unsigned long long)moved<MOVE, ROWS>((uint32_t)(v >> 32), (uint32_t)(none >> 32)) << 32 |
+           moved<MOVE, ROWS>((uint32_t)v, (uint32_t)none);
+}
+template <int MOVE, int ROWS = 15>
+__device__ __forceinline__ double moved(double v, double none)
+{
+    return __longlong_as_double((long long)moved<MOVE, ROWS>((unsigned long long)__double_as_longlong(v),
+                                                             (unsigned long long)__double_as_longlong(none)));
+}
+
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+    auto with = [&](uint32_t other) { v = fmaxf(v, __uint_as_float(other)); };
+    with(moved<kUp1>(__float_as_uint(v), __float_as_uint(v)));
+    with(moved<kUp2>(__float_as_uint(v), __float_as_uint(v)));
+    with(moved<kUp4>(__float_as_uint(v), __float_as_uint(v)));
+    with(moved<kUp8>(__float_as_uint(v), __float_as_uint(v)));
+    with(moved<kRow, 10>(__float_as_uint(v), __float_as_uint(v)));
+    with(moved<kRows, 12>(__float_as_uint(v), __float_as_uint(v)));
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 
 // G groups of eight logits a thread.
@@ -248,17 +275,25 @@ void sample_bins(SampleArgs a, Part *__restrict__ parts, int32_t splits)
     }
 }
 
+// Sum of v over the wave's lanes up to this one.
+template <typename V>
+__device__ __forceinline__ V wave_scan(V v)
+{
+    v += moved<kUp1>(v, V(0));
+    v += moved<kUp2>(v, V(0));
+    v += moved<kUp4>(v, V(0));
+    v += moved<kUp8>(v, V(0));
+    v += moved<kRow, 10>(v, V(0));
+    v += moved<kRows, 12>(v, V(0));
+    return v;
+}
+
 // Sum of v over the threads before this one; `total` over all of them.
 template <int TH, typename V>
 __device__ __forceinline__ V scan(V v, V *part, V &total)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    V s = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const V n = __shfl_up(s, o);
-        s += lane >= o ? n : V(0);
-    }
+    const V s = wave_scan(v);
     __syncthreads();          // part may still be read from the scan before
     if (lane == 63)
         part[wave] = s;
@@ -271,8 +306,7 @@ __device__ __forceinline__ V scan(V v, V *part, V &total)
         before += w < wave ? x : V(0);
         total += x;
     }
-    s = __shfl_up(s, 1);
-    return lane ? before + s : before;
+    return before + moved<kWave1>(s, V(0));
 }
 
 // The first of n <= 4096 places that is right, n - 1 if no other is: `right` turns
@@ -281,9 +315,11 @@ template <typename F>
 __device__ __forceinline__ int first_of(int n, F right)
 {
     const int lane = threadIdx.x & 63;
-    const int at = min(lane * 64 + 63, n - 1);
-    const uint64_t far = __ballot(right(at));
-    const int from = far ? (int)__builtin_ctzll(far) * 64 : 63 * 64;
+    int from = 0;
+    if (n > 64) {
+        const uint64_t far = __ballot(right(min(lane * 64 + 63, n - 1)));
+        from = far ? (int)__builtin_ctzll(far) * 64 : 63 * 64;
+    }
     const uint64_t near = __ballot(right(min(from + lane, n - 1)));
     return min(near ? from + (int)__builtin_ctzll(near) : n - 1, n - 1);
 }
@@ -310,7 +346,7 @@ struct Ranges {
 template <int TH, typename T>
 struct Draw {
     // tokens put in order at a time: as many as LDS holds for one workgroup of 1024 or two of 512 a CU
-    static constexpr int kList = TH == 1024 ? 4096 : 3072;
+    static constexpr int kList = TH == 1024 ? 4096 : 2560;
     static constexpr int kPicked = 2 * kList;
 
     struct Shared {
@@ -328,6 +364,8 @@ struct Draw {
         Ranges r;
         uint32_t listed;
         int32_t least_lo, least_hi;
+        int32_t at[3], place[3];         // bins of top-k, top-p and the draw (-1: not known yet), of their tokens in the list,
+        double edge[3], units[3];        // their edges' weights, units of a bin in a weight of one
     };
     Shared &sh;
     const SampleArgs &a;
@@ -731,46 +769,37 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
     // below the kept weight whatever u
     auto target = [&](double kept) { return fmin((double)u * kept, kept * (1.0 - 0x1p-52)); };
     if (threadIdx.x < 64) {
-        Ranges &r = sh.r;
-        int n = 0;
-        auto want = [&](int lo, int hi) {
-            // in the order of the bins, joined where they meet
-            int i = 0;
-            while (i < n && r.hi[i] < lo)
-                ++i;
-            int j = i;
-            while (j < n && r.lo[j] <= hi) {
-                lo = min(lo, r.lo[j]);
-                hi = max(hi, r.hi[j]);
-                ++j;
-            }
-            if (j == i) {
-                for (int q = n; q > i; --q)
-                    r.lo[q] = r.lo[q - 1], r.hi[q] = r.hi[q - 1];
-                ++n;
-            } else {
-                for (int q = j; q < n; ++q)
-                    r.lo[i + 1 + q - j] = r.lo[q], r.hi[i + 1 + q - j] = r.hi[q];
-                n -= j - i - 1;
-            }
-            r.lo[i] = lo;
-            r.hi[i] = hi;
-        };
+        // the borders' ranges of bins: top-k, top-p, min-p, the draw; from..to -1 where there is none
+        int from[4], to[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            from[i] = kBins, to[i] = -1;
         double wlo = total * kLess, whi = total * kMore;
         int last_bin = kBins - 1, least_lo = kBins;
-        auto kept_within = [&](int lo, int hi) {
-            want(lo, hi);
+        auto kept_within = [&](int i, int lo, int hi) {
+            from[i] = lo;
+            to[i] = hi;
             last_bin = hi;
             wlo = fmin(wlo, sh.wpre[lo] * kLess);
             whi = fmin(whi, sh.wpre[hi + 1] * kMore);
         };
+        // the bins of the weights w0 and w1 >= w0
+        auto bins_of = [&](double w0, double w1, bool past, int &lo, int &hi) {
+            lo = hi = bin_of(1, w0, past);
+            const double x = sh.wpre[lo + 1];
+            if (!(past ? x > w1 : x >= w1))
+                hi = bin_of(1, w1, past);
+        };
+        int at[3] = {-1, -1, -1};        // the bins of top-k, top-p and the draw, where they are known already
         if (by_k) {
-            const int b = bin_of((uint32_t)k, 0.0, false);
-            kept_within(b, b);
+            at[0] = bin_of((uint32_t)k, 0.0, false);
+            kept_within(0, at[0], at[0]);
         }
         if (by_p) {
-            const int lo = min(bin_of(1, p > 0.0f ? (double)p * wlo : 0.0, false), last_bin);
-            kept_within(lo, min(bin_of(1, p > 0.0f ? (double)p * whi : 0.0, false), last_bin));
+            int lo, hi;
+            bins_of(p > 0.0f ? (double)p * wlo : 0.0, p > 0.0f ? (double)p * whi : 0.0, false, lo, hi);
+            at[1] = lo == hi && hi <= last_bin ? lo : -1;
+            kept_within(1, min(lo, last_bin), min(hi, last_bin));
         }
         if (by_least) {
             // exp((l - top) / T) >= min_p from top + T ln(min_p) on, give or take the roundings
@@ -780,25 +809,75 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
             const int first = (int)fmax(0.0, fmin(lo, (double)kBins));
             if (first <= last_bin) {
                 least_lo = first;
-                kept_within(first, min((int)fmin(hi, (double)kBins - 1), last_bin));
+                kept_within(2, first, min((int)fmin(hi, (double)kBins - 1), last_bin));
                 sh.least_hi = last_bin;
             }
         }
-        const int lo = min(bin_of(1, target(wlo), true), last_bin), hi = min(bin_of(1, target(whi), true), last_bin);
-        want(min(lo, hi), hi);
-        uint32_t listed = 0;
-        for (int i = 0; i < n; ++i) {
-            listed += sh.cpre[r.hi[i] + 1] - sh.cpre[r.lo[i]];
-            d.span(r.lo[i], r.hi[i], r.from[i], r.to[i]);
+        int lo, hi;
+        bins_of(target(wlo), target(whi), true, lo, hi);
+        at[2] = lo == hi && hi <= last_bin ? lo : -1;
+        to[3] = min(hi, last_bin);
+        from[3] = min(lo, to[3]);
+        // in the order of the bins, joined where they meet
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass)
+#pragma unroll
+            for (int i = 0; i < 3 - pass; ++i)
+                if (from[i + 1] < from[i]) {
+                    const int f = from[i], e = to[i];
+                    from[i] = from[i + 1], to[i] = to[i + 1];
+                    from[i + 1] = f, to[i + 1] = e;
+                }
+        // lane i: range i
+        const int lane = threadIdx.x;
+        int n = 0, mine_lo = 0, mine_hi = -1;
+        {
+            int f = from[0], e = to[0];
+#pragma unroll
+            for (int i = 1; i < 5; ++i) {
+                const bool more = i < 4 && from[i < 4 ? i : 3] < kBins;
+                if (more && from[i < 4 ? i : 3] <= e) {
+                    e = max(e, to[i < 4 ? i : 3]);
+                } else if (more || i == 4) {
+                    if (lane == n)
+                        mine_lo = f, mine_hi = e;
+                    ++n;
+                    if (more)
+                        f = from[i < 4 ? i : 3], e = to[i < 4 ? i : 3];
+                }
+            }
+        }
+        const uint32_t first = sh.cpre[mine_lo], past = sh.cpre[mine_hi + 1];
+        const uint32_t upto = wave_scan(lane < n ? past - first : 0u);
+        const uint32_t listed = (uint32_t)__builtin_amdgcn_readlane((int)upto, 3);
+        const uint32_t all_of = (uint32_t)__builtin_amdgcn_readlane((int)past, n - 1) - (uint32_t)__builtin_amdgcn_readlane((int)first, 0);
+        // each range costs a comparison with every logit, a token read in vain some more: one range where few lie between
+        const int read = n > 1 && all_of - listed <= (uint32_t)a.vocab / 64 ? 1 : n;
+        Ranges &r = sh.r;
+        if (lane < n) {
+            r.lo[lane] = mine_lo;
+            r.hi[lane] = mine_hi;
+            d.span(mine_lo, mine_hi, r.from[lane], r.to[lane]);
+        }
+        if (read == 1 && lane == n - 1)
+            r.from[0] = r.from[n - 1];
+        uint32_t place[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            place[i] = wave_scan(lane < n ? sh.cpre[min(max(at[i], mine_lo), mine_hi + 1)] - first : 0u);
+        if (lane < 3) {
+            const int b = lane == 0 ? at[0] : lane == 1 ? at[1] : at[2];
+            sh.at[lane] = b;
+            sh.edge[lane] = s.edge_weight(max(b, 0));
+            sh.units[lane] = kOne / sh.edge[lane];
+        }
+        if (lane == 3) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                sh.place[i] = (int)place[i];
         }
         r.n = n;
-        // each range costs a comparison with every logit, a token read in vain some more: one range where few lie between
-        r.read = n;
-        const uint32_t between = sh.cpre[r.hi[n - 1] + 1] - sh.cpre[r.lo[0]] - listed;
-        if (n > 1 && between <= (uint32_t)a.vocab / 64) {
-            r.read = 1;
-            r.from[0] = r.from[n - 1];
-        }
+        r.read = read;
         sh.listed = listed;
         sh.least_lo = least_lo;
     }
@@ -853,8 +932,10 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
 
     // Where the kept tokens end; nothing is looked for past it.
     Border cap{total, kBins, {0, 0}};
-    auto border = [&](uint32_t c, double w, bool past) -> Border {
-        int b = bin_of(c, w, past);
+    // which: 0 top-k, 1 top-p, 2 the draw, 3 min-p
+    auto border = [&](int which, uint32_t c, double w, bool past) -> Border {
+        const bool known = which < 3 && sh.at[which < 3 ? which : 0] >= 0;
+        int b = known ? sh.at[which] : bin_of(c, w, past);
         if (b > cap.bin) {
             if (!past)
                 return cap;
@@ -863,9 +944,10 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         const uint32_t before = sh.cpre[b], n = sh.cpre[b + 1] - before;
         if (c == before + n && !(w > 0.0) && !past)
             return {sh.wpre[b + 1], b, {0, ~0ull}};      // the bin's end, of whatever tokens
-        const double wb = sh.wpre[b], edge = s.edge_weight(b);
+        const bool prepared = known && b == sh.at[which];
+        const double wb = sh.wpre[b], edge = prepared ? sh.edge[which] : s.edge_weight(b);
         // whole units of the bin's weight that the token has to reach, of those that the limits keep
-        double units = (w - wb) / edge * kOne;
+        double units = (w - wb) * (prepared ? sh.units[which] : kOne / edge);
         units = past ? floor(units) + 1.0 : ceil(units);
         Query q;
         q.count = c > before ? c - before : 0;
@@ -875,9 +957,9 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         if (q.count == 0 && q.weight == 0)
             q.count = 1;
         Found f;
-        int at = 0;              // of the bin's tokens in the list
-        bool within = false;
-        for (int i = 0; i < r.n; ++i) {
+        int at = prepared ? sh.place[which] : 0;     // of the bin's tokens in the list
+        bool within = prepared;
+        for (int i = 0; i < (prepared ? 0 : r.n); ++i) {
             at += (int)(sh.cpre[min(max(b, r.lo[i]), r.hi[i] + 1)] - sh.cpre[r.lo[i]]);
             within |= b >= r.lo[i] && b <= r.hi[i];
         }
@@ -912,7 +994,7 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
             kept = cap.weight;
             w = target(kept);
         }
-        const Border e = border(c, w, stage == 3);
+        const Border e = border(stage == 2 ? 3 : min(stage, 2), c, w, stage == 3);
         if (stage == 3)
             entry = e.f.entry;
         else if (e.bin < cap.bin || (e.bin == cap.bin && e.f.weight < cap.f.weight))
