@@ -582,13 +582,20 @@ __global__ __launch_bounds__(256) void int8_join(Int8Args a, int splits, const i
     finish<1, DELTA>(a, t0, count, channel * 16, DELTA ? order_by_variant(a, t0, count) : Order{lane, 0}, b, acc, accd);
 }
 
-// Splits of a call's columns: as many as give each CU two workgroups, of four ranges at least.
+// Splits of a call's columns: as many as give each CU two workgroups, of two ranges
+// at least, or one where each range meets many variants' signs.
+//   us, 64 tokens x 8192 columns, ranges at least    4      2      1
+//     1024 channels, one delta                      18.3   16.0   18.6
+//                    4 variants                     36.1   27.1   26.0
+//                   14                              55.6   36.6   30.9
+//     2048 channels, none                           13.9   13.8   17.2
+//                   14                              57.3   39.9   38.0
 template <int T>
-int mid_splits(int64_t m, int64_t d_out, int64_t d_in)
+int mid_splits(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
     const int64_t groups = (d_out + 63) / 64 * ((m + 16 * T - 1) / (16 * T)), ranges = (d_in + kRange - 1) / kRange;
     int64_t s = 1;
-    while (groups * s < 512 && ranges / (s + 1) >= 4 && s < 16)
+    while (groups * s < 512 && ranges / (s + 1) >= (n_variants >= 8 ? 1 : 2) && s < 16)
         ++s;
     return (int)s;
 }
@@ -604,7 +611,7 @@ template <int T, bool DELTA, bool MANY>
 hipError_t mid(const Int8Args &a, void *workspace, hipStream_t s)
 {
     const int64_t groups = ((a.d_out + 63) / 64 + kXcds - 1) / kXcds * kXcds, blocks = (a.m + 16 * T - 1) / (16 * T);
-    const int splits = mid_splits<T>(a.m, a.d_out, a.d_in);
+    const int splits = mid_splits<T>(a.m, a.n_variants, a.d_out, a.d_in);
     i32x4 *partial = static_cast<i32x4 *>(workspace);
     const dim3 grid((unsigned)(groups * blocks * splits));
     switch (rows_of(a)) {
@@ -620,10 +627,10 @@ hipError_t mid(const Int8Args &a, void *workspace, hipStream_t s)
 }
 
 template <int T>
-size_t mid_workspace(int64_t m, bool delta, int64_t d_out, int64_t d_in)
+size_t mid_workspace(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
-    const int splits = mid_splits<T>(m, d_out, d_in);
-    return splits == 1 ? 0 : (size_t)(splits * ((m + 16 * T - 1) / (16 * T)) * ((d_out + 15) / 16)) * (T * (delta ? 2 : 1) * 64 * 16);
+    const int splits = mid_splits<T>(m, n_variants, d_out, d_in);
+    return splits == 1 ? 0 : (size_t)(splits * ((m + 16 * T - 1) / (16 * T)) * ((d_out + 15) / 16)) * (T * (n_variants ? 2 : 1) * 64 * 16);
 }
 
 template <int NW, bool DELTA, bool MANY>
@@ -638,18 +645,21 @@ hipError_t stream(const Int8Args &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Whether 65 to 128 tokens of many variants go as two lots of 64: a tile has one
-// variant's tokens, few of its rows, and reads all of the base's for them.
-//   us, 100 tokens              tiles   two lots
-//   8192 x 8192, 4 variants        63         74
-//               14                158        128
-//               30 (of 64)        262        177
-//   1024 x 8192, 14                36         52   (too few workgroups)
-//   28672 x 8192, 14              429        469
-bool twice(const Int8Args &a)
+// Whether more than 64 tokens of many variants go in lots of 64: a tile has one
+// variant's tokens, few of its rows, and reads all of the base's for them, a lot
+// reads the base and its variants' signs once.
+//   us                        tiles   lots          tiles   lots
+//                             128 tokens            192 tokens
+//   8192 x 8192, 4 variants      71     80            104    142
+//               14              154    129            158    223
+//               38 of 64        334    198            366    300
+//   1024 x 8192, 14              37     38             43     48
+//   28672 x 8192, 14            422    469            456    653
+//               38 of 64       1023    705           1177    995
+bool in_lots(const Int8Args &a)
 {
-    const int64_t blocks = (a.m + 63) / 64;
-    return a.ids && blocks == 2 && a.n_variants >= 12 && (a.d_out + 63) / 64 * blocks * mid_splits<4>(a.m, a.d_out, a.d_in) >= 256;
+    const int64_t lots = (a.m + 63) / 64;
+    return a.ids && 3 * lots * lots <= (a.n_variants < a.m ? a.n_variants : a.m);
 }
 
 }  // namespace
@@ -663,15 +673,15 @@ size_t linear_int8_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out,
 {
     if (m < kMidFrom)
         return 0;
-    const size_t mid = m <= 32 ? mid_workspace<2>(m, n_variants > 0, d_out, d_in)
-                               : mid_workspace<4>(m, n_variants > 0, d_out, d_in);
+    const size_t mid = m <= 32 ? mid_workspace<2>(m, n_variants, d_out, d_in)
+                               : mid_workspace<4>(m, n_variants, d_out, d_in);
     const size_t tiles = m < kTilesFrom ? 0 : int8_tiles_workspace_bytes(m, n_variants, d_out, d_in);
     return mid > tiles ? mid : tiles;
 }
 
 hipError_t launch_linear_int8(const Int8Args &a, void *workspace, hipStream_t s)
 {
-    if (a.m >= kTilesFrom && !twice(a) && int8_tiles_take(a))
+    if (a.m >= kTilesFrom && !in_lots(a) && int8_tiles_take(a))
         return launch_int8_tiles(a, workspace, s);
     if (a.m < kMidFrom)
         return a.ids ? stream<8, true, true>(a, s) : a.signs ? stream<8, true, false>(a, s) : stream<8, false, false>(a, s);

@@ -1003,8 +1003,12 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
     if (threadIdx.x == 0) {
         a.tokens[row] = (int32_t)entry;
         if (a.logprobs) {
-            const double z = s.alone || s.flat ? 0.0 : ((double)logit_of(~(uint32_t)(entry >> 32)) - (double)top) / s.t;
-            a.logprobs[row] = (float)(z - log(kept));
+#pragma clang fp contract(off)
+            // from the weight as it stands in the sums, rounded alike: what else is kept is so right next to a
+            // probability of one too, and nothing where the token is kept alone
+            const float l = logit_of(~(uint32_t)(entry >> 32));
+            const double w = (double)s.weight(l) * (1.0 / kOne) * s.edge_weight((int)s.bin(l));
+            a.logprobs[row] = (float)(0.0 - log1p(fmax(kept - w, 0.0) / w));
         }
     }
 }

@@ -205,3 +205,33 @@ def test_draws_follow_the_probabilities(bd):
     tokens, _ = bd.sample(l.expand(n, 300).contiguous().to(DEV), u.float().to(DEV), temperature=0.9)
     p = torch.softmax(l[0].double() / 0.9, 0)
     assert ((torch.bincount(tokens.cpu().long(), minlength=300) - p * n).abs() <= 1.0 + n * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t", [0.3, 0.7, 1.0, 3.0])
+def test_a_token_kept_alone_has_logprob_zero(bd, t, dtype):
+    g = torch.Generator().manual_seed(17)
+    for vocab in (1, 2, 500, 40000):
+        logits = torch.randn(9, vocab, generator=g) * 2
+        logits[torch.arange(9), torch.randint(0, vocab, (9,), generator=g)] = 9.3
+        logits, u = logits.to(dtype).cuda(), torch.rand(9, generator=g).cuda()
+        for limit in (dict(top_k=1), dict(top_p=0.0), dict(top_p=1e-5), dict(min_p=1.0), dict(top_k=1, top_p=0.5, min_p=0.9)):
+            tokens, logprobs = bd.sample(logits, u, temperature=t, **limit)
+            assert torch.equal(tokens.long(), logits.argmax(1)) and (logprobs == 0).all()
+
+
+@pytest.mark.parametrize("gap", [1.0, 3.0, 8.0, 14.0, 20.0, 25.0])
+def test_logprob_next_to_a_probability_of_one(bd, gap):
+    g = torch.Generator().manual_seed(18)
+    logits = torch.randn(40, 7, generator=g)
+    logits[:, 3] = logits.max(1).values + gap
+    tokens, logprobs = bd.sample(logits.cuda(), torch.zeros(40).cuda())
+    assert (tokens == 3).all()
+    l = logits.double()
+    others = torch.exp(l - l[:, 3:4])
+    others[:, 3] = 0
+    others = others.sum(1)
+    want = -torch.log1p(others)
+    # the weights are off by 2^-37, the sums by a rounding in 64 bits, the output by half a step of fp32
+    bound = others * 2.0 ** -35 + 8 * 2.0 ** -53 + want.abs() * 2.0 ** -24
+    assert ((logprobs.cpu().double() - want).abs() <= bound).all()
