@@ -669,20 +669,46 @@ bool in_lots(const Int8Args &a)
 // 21 us, 24 tokens 23, 64 tokens 31, 65 tokens 33.
 constexpr int64_t kMidFrom = 17, kTilesFrom = 65;
 
+// Where the tiles do not take more than kSlice tokens they go by slices: a launch
+// has fewer than 2^32 threads.
+constexpr int64_t kSlice = 1 << 20;
+
 size_t linear_int8_workspace_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
     if (m < kMidFrom)
         return 0;
+    size_t most = m < kTilesFrom ? 0 : int8_tiles_workspace_bytes(m, n_variants, d_out, d_in);
+    if (m > kSlice) {
+        for (const int64_t slice : {kSlice, m % kSlice}) {
+            const size_t bytes = linear_int8_workspace_bytes(slice, n_variants, d_out, d_in);
+            most = most > bytes ? most : bytes;
+        }
+        return most;
+    }
     const size_t mid = m <= 32 ? mid_workspace<2>(m, n_variants, d_out, d_in)
                                : mid_workspace<4>(m, n_variants, d_out, d_in);
-    const size_t tiles = m < kTilesFrom ? 0 : int8_tiles_workspace_bytes(m, n_variants, d_out, d_in);
-    return mid > tiles ? mid : tiles;
+    return mid > most ? mid : most;
 }
 
 hipError_t launch_linear_int8(const Int8Args &a, void *workspace, hipStream_t s)
 {
     if (a.m >= kTilesFrom && !in_lots(a) && int8_tiles_take(a))
         return launch_int8_tiles(a, workspace, s);
+    if (a.m > kSlice) {
+        for (int64_t t = 0; t < a.m; t += kSlice) {
+            Int8Args part = a;
+            part.m = a.m - t < kSlice ? a.m - t : kSlice;
+            part.q += t * a.d_in;
+            part.q_scale += t;
+            if (a.ids)
+                part.ids += t;
+            part.y = static_cast<char *>(a.y) + t * a.d_out * (a.f32 ? 4 : 2);
+            const hipError_t e = launch_linear_int8(part, workspace, s);
+            if (e != hipSuccess)
+                return e;
+        }
+        return hipSuccess;
+    }
     if (a.m < kMidFrom)
         return a.ids ? stream<8, true, true>(a, s) : a.signs ? stream<8, true, false>(a, s) : stream<8, false, false>(a, s);
     if (a.m <= 32)

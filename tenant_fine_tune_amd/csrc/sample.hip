@@ -1046,21 +1046,45 @@ void start(const SampleArgs &a, Part *parts, hipStream_t s)
         sample_draw<512, T><<<(unsigned)a.m, 512, 0, s>>>(a, parts, splits);
 }
 
+// Rows go by slices whose bins take 2^28 bytes and a little.
+int64_t slice_rows(int64_t vocab)
+{
+    return ((1 << 28) / (int64_t)sizeof(Part)) / ((vocab + 4 * 8 * kBinThreads - 1) / (4 * 8 * kBinThreads));
+}
+
 }  // namespace
 
 size_t sample_workspace_bytes(int64_t m, int64_t vocab)
 {
-    return (size_t)(m * parts_of(m, vocab)) * sizeof(Part);
+    const int64_t slice = slice_rows(vocab), first = m < slice ? m : slice, last = m < slice ? m : m % slice;
+    const int64_t most = first * parts_of(first, vocab), tail = last * parts_of(last, vocab);
+    return (size_t)(most > tail ? most : tail) * sizeof(Part);
 }
 
-hipError_t launch_sample(const SampleArgs &a, void *workspace, hipStream_t s)
+hipError_t launch_sample(const SampleArgs &args, void *workspace, hipStream_t s)
 {
     Part *parts = static_cast<Part *>(workspace);
-    if (a.f32)
-        start<float>(a, parts, s);
-    else
-        start<uint16_t>(a, parts, s);
-    return hipGetLastError();
+    const int64_t slice = slice_rows(args.vocab);
+    for (int64_t row = 0; row < args.m; row += slice) {
+        SampleArgs a = args;
+        a.m = args.m - row < slice ? args.m - row : slice;
+        a.logits = static_cast<const char *>(args.logits) + row * args.stride * (args.f32 ? 4 : 2);
+        a.u += row;
+        a.tokens += row;
+        a.temperature = args.temperature ? args.temperature + row : nullptr;
+        a.top_k = args.top_k ? args.top_k + row : nullptr;
+        a.top_p = args.top_p ? args.top_p + row : nullptr;
+        a.min_p = args.min_p ? args.min_p + row : nullptr;
+        a.logprobs = args.logprobs ? args.logprobs + row : nullptr;
+        if (a.f32)
+            start<float>(a, parts, s);
+        else
+            start<uint16_t>(a, parts, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace bd

@@ -207,3 +207,29 @@ def test_linear_of_quantized_rows_is_near_the_product(bd):
     dx, dw = s.cpu().double()[:, None] / 2, cs.cpu().double()[:, None] / 2
     bound = dx * w.abs().sum(1) + x.abs().sum(1)[:, None] * dw.T + 512 * dx * dw.T
     assert ((y - x @ w.T).abs() <= bound * (1 + 2.0 ** -20)).all()
+
+
+@pytest.mark.parametrize("variants", [0, 3])
+def test_linear_more_tokens_than_a_launch_takes(bd, variants):
+    # rows that end inside 32 columns and too many to copy: slices, the last of them short
+    for m in ((1 << 23) + 5, (1 << 23) + (1 << 20) + 40):
+        linear_matches(bd, ref.random_case(m, 2, 8, variants, 3), out_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("m", [65, 100, 128, 129, 192, 300])
+@pytest.mark.parametrize("variants", [13, 40, 200])
+def test_linear_many_variants_in_lots(bd, m, variants):
+    linear_matches(bd, ref.random_case(m, 130, 1056, variants, m), out_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("m,n,k", [(70, 130, 40), (333, 1000, 4104), (130, 257, 1032), (65, 1, 8), (90, 64, 8200)])
+@pytest.mark.parametrize("variants", [0, 1, 3, 16])
+def test_linear_rows_that_end_inside_32_columns(bd, m, n, k, variants):
+    linear_matches(bd, ref.random_case(m, n, k, variants, k), out_dtype=torch.float32)
+    linear_matches(bd, ref.random_case(m, n, k, variants, k + 1, extremes=True))
+
+
+@pytest.mark.parametrize("m,n,k", [(80, 2048, 8192), (512, 512, 16384), (1000, 300, 8192), (200, 4096, 2048)])
+@pytest.mark.parametrize("variants", [0, 1, 3])
+def test_linear_split_columns(bd, m, n, k, variants):
+    linear_matches(bd, ref.random_case(m, n, k, variants, m), out_dtype=torch.float32)

@@ -235,3 +235,18 @@ def test_logprob_next_to_a_probability_of_one(bd, gap):
     # the weights are off by 2^-37, the sums by a rounding in 64 bits, the output by half a step of fp32
     bound = others * 2.0 ** -35 + 8 * 2.0 ** -53 + want.abs() * 2.0 ** -24
     assert ((logprobs.cpu().double() - want).abs() <= bound).all()
+
+
+def test_more_rows_than_the_scratch_holds_at_once(bd):
+    m, vocab = 40000, 33
+    g = torch.Generator().manual_seed(19)
+    logits, u = torch.randn(m, vocab, generator=g), torch.rand(m, generator=g)
+    k, t = torch.randint(0, 9, (m,), generator=g).int(), torch.rand(m, generator=g) + 0.1
+    assert bd.lib.bitdelta_sample_workspace(m, vocab) <= 2 ** 28 + 2 ** 24
+    tokens, logprobs = bd.sample(logits.cuda(), u.cuda(), top_k=k.cuda(), temperature=t.cuda(), top_p=0.95, min_p=0.01)
+    for at in (0, 16300, 16380, 32760, m - 20):     # either side of where a slice ends, and both ends
+        s = slice(at, at + 20)
+        ref.check(tokens[s], logprobs[s], logits[s], u[s], t[s], k[s], torch.full((20,), 0.95), torch.full((20,), 0.01))
+    again = bd.sample(logits[20000:30000].cuda(), u[20000:30000].cuda(), top_k=k[20000:30000].cuda(),
+                      temperature=t[20000:30000].cuda(), top_p=0.95, min_p=0.01)
+    assert torch.equal(again[0], tokens[20000:30000]) and torch.equal(again[1], logprobs[20000:30000])

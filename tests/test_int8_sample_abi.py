@@ -113,7 +113,7 @@ def test_sample_workspace_over_its_range(bd):
     for m in (1, 7, 512, MAX_ROWS):
         for vocab in (1, 8192, 50257, MAX_VOCAB):
             need = ask(m, vocab)
-            assert need > 0
+            assert 0 < need <= 2 ** 28 + 2 ** 24
             assert draw(bd, m=m, vocab=vocab, ls=vocab, nws=need - 1) == bd.BD_EWORKSPACE
 
 
