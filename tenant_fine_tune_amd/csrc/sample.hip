@@ -776,13 +776,19 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
             from[i] = kBins, to[i] = -1;
         double wlo = total * kLess, whi = total * kMore;
         int last_bin = kBins - 1, least_lo = kBins;
-        auto kept_within = [&](int i, int lo, int hi) {
+        // the weight kept ends in the bins lo .. hi, and within [least, most]
+        auto kept_within = [&](int i, int lo, int hi, double least, double most) {
             from[i] = lo;
             to[i] = hi;
             last_bin = hi;
-            wlo = fmin(wlo, sh.wpre[lo] * kLess);
-            whi = fmin(whi, sh.wpre[hi + 1] * kMore);
+            wlo = fmin(wlo, fmax(sh.wpre[lo], least) * kLess);
+            whi = fmin(whi, fmin(sh.wpre[hi + 1], most) * kMore);
         };
+        // A bin's tokens differ by exp(1/32) at most, the heaviest stand first: what the
+        // first of them weigh in the mean, at least and at most.  With bounds as near as
+        // this the next border is in one bin nearly always, and all borders' tokens fit the list.
+        constexpr double kLightest = 1.0 - 0x1p-30, kHeaviest = 1.04;
+        auto mean_of = [&](int b) { return (sh.wpre[b + 1] - sh.wpre[b]) / (double)max(sh.cpre[b + 1] - sh.cpre[b], 1u); };
         // the bins of the weights w0 and w1 >= w0
         auto bins_of = [&](double w0, double w1, bool past, int &lo, int &hi) {
             lo = hi = bin_of(1, w0, past);
@@ -793,13 +799,17 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         int at[3] = {-1, -1, -1};        // the bins of top-k, top-p and the draw, where they are known already
         if (by_k) {
             at[0] = bin_of((uint32_t)k, 0.0, false);
-            kept_within(0, at[0], at[0]);
+            const double first = (double)((uint32_t)k - sh.cpre[at[0]]) * mean_of(at[0]);
+            kept_within(0, at[0], at[0], sh.wpre[at[0]] + first * kLightest, sh.wpre[at[0]] + first * kHeaviest);
         }
         if (by_p) {
+            const double w0 = p > 0.0f ? (double)p * wlo : 0.0, w1 = p > 0.0f ? (double)p * whi : 0.0;
             int lo, hi;
-            bins_of(p > 0.0f ? (double)p * wlo : 0.0, p > 0.0f ? (double)p * whi : 0.0, false, lo, hi);
+            bins_of(w0, w1, false, lo, hi);
             at[1] = lo == hi && hi <= last_bin ? lo : -1;
-            kept_within(1, min(lo, last_bin), min(hi, last_bin));
+            lo = min(lo, last_bin);
+            // up to one token past what is asked for
+            kept_within(1, lo, min(hi, last_bin), w0, w1 + mean_of(lo) * kHeaviest);
         }
         if (by_least) {
             // exp((l - top) / T) >= min_p from top + T ln(min_p) on, give or take the roundings
@@ -809,7 +819,7 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
             const int first = (int)fmax(0.0, fmin(lo, (double)kBins));
             if (first <= last_bin) {
                 least_lo = first;
-                kept_within(2, first, min((int)fmin(hi, (double)kBins - 1), last_bin));
+                kept_within(2, first, min((int)fmin(hi, (double)kBins - 1), last_bin), 0.0, INFINITY);
                 sh.least_hi = last_bin;
             }
         }
