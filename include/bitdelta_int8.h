@@ -26,7 +26,7 @@ extern "C" {
  * infinity gives scale NaN and zeros, so that it stays visible in what is
  * computed from it.  q: int8 [m, d] dense, scale: fp32 [m].  The same call
  * serves activations (rows are tokens) and weights (rows are output channels).
- * Element alignment is enough for x and q.  1 <= d <= BD_INT8_MAX_WIDTH. */
+ * Element alignment is enough for x and q, which do not overlap.  1 <= d <= BD_INT8_MAX_WIDTH. */
 #define BD_INT8_MAX_WIDTH 131064
 
 BD_API bd_status bitdelta_quantize_int8(const void *x, int64_t x_stride, int x_dtype, int64_t m, int64_t d, int8_t *q,
@@ -50,7 +50,8 @@ BD_API bd_status bitdelta_quantize_int8(const void *x, int64_t x_stride, int x_d
  * d_in: a multiple of 8, at most BD_INT8_MAX_WIDTH; q, w, one variant's signs and y
  * each below 2 GiB.
  * workspace: at least bitdelta_linear_int8_workspace() bytes, 16-byte aligned,
- * scratch (n_variants as in the call, 0 without deltas).  The result does not depend
+ * scratch (n_variants as in the call, 0 without deltas); at most 2^29 bytes and what
+ * a table of the tokens takes.  y and workspace overlap nothing else.  The result does not depend
  * on how a call is cut, nor on its other tokens: sums of whole numbers are exact in any order. */
 BD_API size_t bitdelta_linear_int8_workspace(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in);
 BD_API bd_status bitdelta_linear_int8(const int8_t *q, const float *q_scale, int64_t m, const int8_t *w,

@@ -31,13 +31,16 @@ extern "C" {
  * logprob -inf.
  * Weights are held to within 2^-37 of themselves, in whole numbers whose sums are
  * exact, so the result does not depend on how a row is cut; a token below exp(-32)
- * of the first may count as one without weight.
+ * of the first may count as one without weight.  logprob is formed from what is
+ * kept beside the token drawn: near 0 it is right to about 2^-35 of itself, and 0
+ * where the token is kept alone.
  * logits: [m, vocab] of logits_dtype (BD_BF16 or BD_F32), row stride in elements
  * (>= vocab), element alignment; u: fp32 [m]; temperature, top_p, min_p fp32 [m],
  * top_k int32 [m], each NULL for the call's one value *_all.  tokens: int32 [m],
  * logprobs: fp32 [m] or NULL.
  * 1 <= vocab <= BD_SAMPLE_MAX_VOCAB, m <= BD_SAMPLE_MAX_ROWS (BD_ESHAPE otherwise).  workspace: at least
- * bitdelta_sample_workspace() bytes, 16-byte aligned, scratch. */
+ * bitdelta_sample_workspace() bytes, 16-byte aligned, scratch; little more than 2^28
+ * bytes at most.  Outputs and workspace overlap nothing else. */
 #define BD_SAMPLE_MAX_VOCAB 1048576
 #define BD_SAMPLE_MAX_ROWS 131072
 

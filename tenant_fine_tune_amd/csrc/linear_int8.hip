@@ -142,6 +142,8 @@ __device__ __forceinline__ void finish(const Int8Args &a, int64_t t0, int count,
 // The tokens are ordered by variant; a variant's product is formed for all 16 and
 // kept for its own.
 // MANY: with variant ids.
+// One token through 8192 x 8192 with one delta 14.9 us, 5.1 TB/s; 16 of 14 variants
+// through 10240 x 8192 50 us, 3.6 TB/s, between the variants' 64-byte pieces of rows.
 template <int NW, bool DELTA, bool MANY, Rows R>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4)))
 void int8_stream(Int8Args a)
@@ -336,6 +338,9 @@ void int8_stream(Int8Args a)
 // ranges, which share lines of signs, are read on one die at a time.  All waves
 // work on one range and share the tokens' numbers in LDS; the signs of the
 // following variants, the next range's among them, are on their way while one is used.
+// 32 tokens through 50257 x 8192 without a delta 93 us, 4.4 TB/s; 61 tokens of 14
+// variants through 8192 x 28672 223 us and the join 9.5, 2.8 TB/s: spreading signs to
+// bytes is 45% of the vector instructions' time, and lines of signs are fetched twice.
 constexpr int kMidWaves = 4;
 
 template <int T, bool DELTA, bool MANY, Rows R>

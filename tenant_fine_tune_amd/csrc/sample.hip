@@ -17,9 +17,14 @@
 // Bins are d = 2^e wide, T / 64 < d <= T / 32, at multiples of d, so the parts' bins
 // are the same ones; 2048 of them reach exp(-32) below the part's largest logit, and
 // what lies deeper has no weight.  In a bin with lower edge L the weight relative to
-// it, exp((l - L) / T), exceeds one by 1/32 at most; that excess, held in units of
+// it, exp((l - L) / T), exceeds one by exp(1/32) - 1 at most; that excess, held in units of
 // 2^-36, and the count share a 64-bit number, so that one LDS addition serves both,
 // and all sums are of whole numbers: exact, in any order, cut in any way.
+//
+// sample_bins is bound by its vector instructions and LDS additions, one of 64 bits a
+// logit: 512 rows of 131071 bf16 logits 51 us (2.6 TB/s), one of 32000 4.2.  sample_draw
+// is bound by its stages, each waiting for the one before: one row 14 us, of which the
+// row's reading takes 2; 512 rows 52 to 56, of which 15 are the reading from the caches.
 #include "bd_device.h"
 #include "sample_launch.h"
 
@@ -28,7 +33,7 @@ namespace {
 
 constexpr int kBinThreads = 1024;            // of sample_bins
 constexpr int kBins = 2048;
-constexpr int kCountShift = 47;              // of a packed bin: below it 65536 tokens' excess, each below 2^31
+constexpr int kCountShift = 47;              // of a packed bin: below it the excess of a part's tokens (32768 at most), each below 2^32
 constexpr uint64_t kExcess = (1ull << kCountShift) - 1;
 constexpr uint32_t kWithoutExponents = 0x9DA1u;   // inverse of 1 + 0x433 * 2^5 of 2^17
 constexpr double kOne = 0x1p36;              // weight of a token at its bin's lower edge
@@ -1050,7 +1055,9 @@ void start(const SampleArgs &a, Part *parts, hipStream_t s)
     default: sample_bins<1, T><<<grid, kBinThreads, 0, s>>>(a, parts, splits); break;
     }
     // up to a row a CU the wider form is faster; of more rows one is at its borders while another is read
-    if (a.m <= 256)
+    // (512 rows of 131071 bf16 logits 106 us, by the wider form 114), as long as the shorter list holds the
+    // tokens of three full bins (three limits among the likely tokens, 300 rows of 220000: 308 us, 188 by the wider form)
+    if (a.m <= 256 || a.vocab > 150000)
         sample_draw<1024, T><<<(unsigned)a.m, 1024, 0, s>>>(a, parts, splits);
     else
         sample_draw<512, T><<<(unsigned)a.m, 512, 0, s>>>(a, parts, splits);
