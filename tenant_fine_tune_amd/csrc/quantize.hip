@@ -4,7 +4,8 @@
 //
 // One workgroup per row keeps the row in registers between the maximum and the
 // quotients: every input is read once, memory bound.  2049 x 28672 bf16 44 us,
-// 4.0 TB/s; 4 x 8192 3.9 us, a launch and one trip to memory.
+// 4.0 TB/s; 4 x 8192 3.9 us, a launch and one trip to memory.  Rows too wide for that
+// (above 32768) are read twice: 1024 x 131064 bf16 112 us (held whole, with spills, 146).
 #include "bd_device.h"
 #include "decoder_launch.h"
 #include "int8_launch.h"
@@ -95,48 +96,29 @@ __device__ __forceinline__ float nearest(float x, float s, float inv)
     return t;
 }
 
-// C groups of eight columns a thread.
-template <int C, typename T>
-__global__ __launch_bounds__(1024) void quantize_rows(const T *__restrict__ x, int64_t stride, int64_t m, int d,
-                                                      int8_t *__restrict__ q, float *__restrict__ scale)
-{
-    __shared__ uint32_t part[16];
-    const int64_t i = blockIdx.y * kTokensAcross + blockIdx.x;
-    if (i >= m)
-        return;
-    const int step = blockDim.x * 8, at0 = threadIdx.x * 8;
-    const T *row = x + i * stride;
-    Eight<T> v[C];
-    uint32_t top = 0;   // as bits: an infinity is above every number, a NaN above that
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-        v[c].load(row + at0 + c * step, min(max(d - at0 - c * step, 0), 8));
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            top = max(top, __float_as_uint(v[c].get(j)) & 0x7FFFFFFFu);
-    top = max_all(top, part);
-    const bool finite = top < 0x7F800000u;
-    const float s = finite ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7FC00000u);
-    if (threadIdx.x == 0)
-        scale[i] = s;
-    const bool zero = !(s > 0.0f);
-    const float inv = 1.0f / s;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int at = at0 + c * step, n = min(max(d - at, 0), 8);
+// The row's scale from the bits of its largest magnitude (an infinity is above every
+// number, a NaN above that), and its quotients.
+struct Quotients {
+    float s, inv;
+    __device__ __forceinline__ explicit Quotients(uint32_t top)
+    {
+        s = top < 0x7F800000u ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7FC00000u);
+        inv = 1.0f / s;
+    }
+    // Eight numbers, n of which exist.
+    template <typename T>
+    __device__ __forceinline__ void store(const Eight<T> &v, int8_t *p, int n) const
+    {
         uint32_t b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float t;
             if (s < kTinyScale)   // 1/s may not exist in fp32; of 24-bit numbers the fp64 quotient rounds to a half only where it is one
-                t = (float)rint((double)v[c].get(j) / (double)s);
+                t = (float)rint((double)v.get(j) / (double)s);
             else
-                t = nearest(v[c].get(j), s, inv);
-            b[j] = zero ? 0u : (uint32_t)(int)fminf(fmaxf(t, -127.0f), 127.0f) & 0xFFu;
+                t = nearest(v.get(j), s, inv);
+            b[j] = s > 0.0f ? (uint32_t)(int)fminf(fmaxf(t, -127.0f), 127.0f) & 0xFFu : 0u;
         }
-        int8_t *p = q + i * d + at;
         if (n == 8) {
             typedef uint32_t u32x2a1 __attribute__((ext_vector_type(2), aligned(1)));
             *reinterpret_cast<u32x2a1 *>(p) = (u32x2a1){b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24,
@@ -148,14 +130,60 @@ __global__ __launch_bounds__(1024) void quantize_rows(const T *__restrict__ x, i
                     p[j] = (int8_t)b[j];
         }
     }
+};
+
+// C groups of eight columns a thread and turn, the row in one turn unless WIDE: then
+// it is read a second time for the quotients.
+template <int C, bool WIDE, typename T>
+__global__ __launch_bounds__(1024) void quantize_rows(const T *__restrict__ x, int64_t stride, int64_t m, int d,
+                                                      int8_t *__restrict__ q, float *__restrict__ scale)
+{
+    __shared__ uint32_t part[16];
+    const int64_t i = blockIdx.y * kTokensAcross + blockIdx.x;
+    if (i >= m)
+        return;
+    const int step = blockDim.x * 8, at0 = threadIdx.x * 8;
+    const T *row = x + i * stride;
+    int8_t *out = q + i * d;
+    Eight<T> v[C];
+    uint32_t top = 0;
+    auto load = [&](int from) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            v[c].load(row + from + at0 + c * step, min(max(d - from - at0 - c * step, 0), 8));
+    };
+    int from = 0;
+    do {
+        load(from);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                top = max(top, __float_as_uint(v[c].get(j)) & 0x7FFFFFFFu);
+        from += C * step;
+    } while (WIDE && from < d);
+    const Quotients quotients(max_all(top, part));
+    if (threadIdx.x == 0)
+        scale[i] = quotients.s;
+    // the last turn's columns are still here
+    do {
+        from -= C * step;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = from + at0 + c * step;
+            quotients.store(v[c], out + at, min(max(d - at, 0), 8));
+        }
+        if (WIDE && from > 0)
+            load(from - C * step);
+    } while (WIDE && from > 0);
 }
 
-template <int C, typename T>
+template <int C, bool WIDE, typename T>
 void start(const void *x, int64_t stride, int64_t m, int64_t d, int8_t *q, float *scale, hipStream_t s)
 {
-    const int threads = (int)((d + 512 * C - 1) / (512 * C)) * 64;
+    const int threads = WIDE ? 1024 : (int)((d + 512 * C - 1) / (512 * C)) * 64;
     const dim3 grid((unsigned)(m < kTokensAcross ? m : kTokensAcross), (unsigned)((m + kTokensAcross - 1) / kTokensAcross));
-    quantize_rows<C, T><<<grid, threads, 0, s>>>(static_cast<const T *>(x), stride, m, (int)d, q, scale);
+    quantize_rows<C, WIDE, T><<<grid, threads, 0, s>>>(static_cast<const T *>(x), stride, m, (int)d, q, scale);
 }
 
 template <typename T>
@@ -163,13 +191,13 @@ void start(const void *x, int64_t stride, int64_t m, int64_t d, int8_t *q, float
 {
     // as many waves as the row has groups of 512 C columns, at most 16
     if (d <= 2048)
-        start<1, T>(x, stride, m, d, q, scale, s);
+        start<1, false, T>(x, stride, m, d, q, scale, s);
     else if (d <= 16384)
-        start<2, T>(x, stride, m, d, q, scale, s);
+        start<2, false, T>(x, stride, m, d, q, scale, s);
     else if (d <= 32768)
-        start<4, T>(x, stride, m, d, q, scale, s);
+        start<4, false, T>(x, stride, m, d, q, scale, s);
     else
-        start<16, T>(x, stride, m, d, q, scale, s);
+        start<4, true, T>(x, stride, m, d, q, scale, s);
 }
 
 }  // namespace

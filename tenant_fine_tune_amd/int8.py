@@ -46,12 +46,12 @@ def quantize_int8(x, *, out=None, scale_out=None):
         xp, xs = _dense(x, xt, "x", x.shape, dev), d
         m = x.numel() // d if d else 0
     if out is None:
-        out = torch.empty(x.shape, dtype=_I8, device=x.device)
+        out = torch.empty_like(x, dtype=_I8, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
         op = _dense(out, _I8, "out", x.shape, dev)
     if scale_out is None:
-        scale_out = torch.empty(lead, dtype=_F32, device=x.device)
+        scale_out = x.new_empty(lead, dtype=_F32)
         sp = scale_out.data_ptr()
     else:
         sp = _dense(scale_out, _F32, "scale_out", lead, dev)
@@ -114,13 +114,13 @@ def linear_int8(q, q_scale, weight, weight_scale, delta_sign=None, alpha=None, *
     if out is None:
         if out_dtype is not _BF16 and out_dtype is not _F32:
             raise TypeError("out_dtype must be bfloat16 or float32")
-        out = torch.empty((*lead, d_out), dtype=out_dtype, device=q.device)
+        out = q.new_empty((*lead, d_out), dtype=out_dtype)
         op = out.data_ptr()
     else:
         out_dtype = out.dtype if isinstance(out, _Tensor) and out.dtype is _F32 else _BF16
         op = _dense(out, out_dtype, "out", (*lead, d_out), dev)
     nws = lib.bitdelta_linear_int8_workspace(m, variants, d_out, d_in)
-    ws = torch.empty((nws,), dtype=_U8, device=q.device) if nws else None
+    ws = q.new_empty((nws,), dtype=_U8) if nws else None
     with _on(dev):
         status = lib.bitdelta_linear_int8(qp, sp, m, wp, cp, dp, ap, mode, ip, variants, d_out, d_in, op,
                                           BD_F32 if out_dtype is _F32 else BD_BF16, ws.data_ptr() if nws else 0, nws,

@@ -56,17 +56,17 @@ def sample(logits, u, *, temperature=1.0, top_k=None, top_p=None, min_p=None, ou
     pp, p = _each(1.0 if top_p is None else top_p, _F32, "top_p", m, dev)
     np_, n = _each(0.0 if min_p is None else min_p, _F32, "min_p", m, dev)
     if out is None:
-        out = torch.empty((m,), dtype=_I32, device=logits.device)
+        out = logits.new_empty((m,), dtype=_I32)
         op = out.data_ptr()
     else:
         op = _dense(out, _I32, "out", (m,), dev)
     if logprobs_out is None:
-        logprobs_out = torch.empty((m,), dtype=_F32, device=logits.device)
+        logprobs_out = logits.new_empty((m,), dtype=_F32)
         gp = logprobs_out.data_ptr()
     else:
         gp = _dense(logprobs_out, _F32, "logprobs_out", (m,), dev)
     nws = lib.bitdelta_sample_workspace(m, vocab)
-    ws = torch.empty((nws,), dtype=torch.uint8, device=logits.device) if nws else None
+    ws = logits.new_empty((nws,), dtype=torch.uint8) if nws else None
     with _on(dev):
         status = lib.bitdelta_sample(lp, ls, BD_F32 if dtype is _F32 else BD_BF16, m, vocab, up, tp, t, kp, k, pp, p, np_, n,
                                      op, gp, ws.data_ptr() if nws else 0, nws, _stream(dev))
