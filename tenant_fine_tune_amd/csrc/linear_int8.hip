@@ -339,8 +339,8 @@ void int8_stream(Int8Args a)
 // work on one range and share the tokens' numbers in LDS; the signs of the
 // following variants, the next range's among them, are on their way while one is used.
 // 32 tokens through 50257 x 8192 without a delta 93 us, 4.4 TB/s; 61 tokens of 14
-// variants through 8192 x 28672 223 us and the join 9.5, 2.8 TB/s: spreading signs to
-// bytes is 45% of the vector instructions' time, and lines of signs are fetched twice.
+// variants through 8192 x 28672 209 us with the join, 3.0 TB/s: signs are spread to bytes
+// by vector instructions, two waves a SIMD hide little, and lines of signs are fetched twice.
 constexpr int kMidWaves = 4;
 
 template <int T, bool DELTA, bool MANY, Rows R>
@@ -412,9 +412,11 @@ void int8_mid(Int8Args a, int splits, i32x4 *__restrict__ partial)
     }
     const unsigned all = (unsigned)((K + kRange - 1) / kRange);
 
-    // A stream of signs over variants and ranges, kAhead of them on their way; a
-    // range's variants are filled up to whole turns of the ring with empty ones.
-    constexpr int kAhead = 3;
+    // A stream of signs over variants and ranges, kAhead of them on their way (more
+    // cost registers: 61 tokens of 14 variants through 8192 x 28672 209 us with one or
+    // two, 233 with three, 245 with five); a range's variants are filled up to whole
+    // turns of the ring with empty ones.
+    constexpr int kAhead = T == 4 ? 1 : 2;
     struct Signs {
         u32x4 s;
         int begin, end;
@@ -589,7 +591,7 @@ __global__ __launch_bounds__(256) void int8_join(Int8Args a, int splits, const i
 
 // Splits of a call's columns: as many as give each CU two workgroups, of two ranges
 // at least, or one where each range meets many variants' signs.
-//   us, 64 tokens x 8192 columns, ranges at least    4      2      1
+//   us, 64 tokens x 8192 columns, ranges at least    4      2      1   (with three loads of signs ahead)
 //     1024 channels, one delta                      18.3   16.0   18.6
 //                    4 variants                     36.1   27.1   26.0
 //                   14                              55.6   36.6   30.9
@@ -655,12 +657,12 @@ hipError_t stream(const Int8Args &a, hipStream_t s)
 // reads the base and its variants' signs once.
 //   us                        tiles   lots          tiles   lots
 //                             128 tokens            192 tokens
-//   8192 x 8192, 4 variants      71     80            104    142
-//               14              154    129            158    223
-//               38 of 64        334    198            366    300
-//   1024 x 8192, 14              37     38             43     48
-//   28672 x 8192, 14            422    469            456    653
-//               38 of 64       1023    705           1177    995
+//   8192 x 8192, 4 variants      71     72            104    108
+//               14              154    122            158    195
+//               38 of 64        334    186            366    305
+//   1024 x 8192, 14              37     35             43     43
+//   28672 x 8192, 14            422    408            456    555
+//               38 of 64       1023    673           1177    941
 bool in_lots(const Int8Args &a)
 {
     const int64_t lots = (a.m + 63) / 64;
