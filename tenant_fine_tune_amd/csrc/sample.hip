@@ -27,16 +27,13 @@
 // row's reading takes 2; 512 rows 52 to 56, of which 15 are the reading from the caches.
 #include "bd_device.h"
 #include "sample_launch.h"
+#include "sample_scale.h"
 
 namespace bd {
 namespace {
 
 constexpr int kBinThreads = 1024;            // of sample_bins
-constexpr int kBins = 2048;
-constexpr int kCountShift = 47;              // of a packed bin: below it the excess of a part's tokens (32768 at most), each below 2^32
-constexpr uint64_t kExcess = (1ull << kCountShift) - 1;
 constexpr uint32_t kWithoutExponents = 0x9DA1u;   // inverse of 1 + 0x433 * 2^5 of 2^17
-constexpr double kOne = 0x1p36;              // weight of a token at its bin's lower edge
 constexpr int kFew = 128;
 
 typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
@@ -81,71 +78,6 @@ struct Eight<float> {
 
 __device__ __forceinline__ float one_of(const uint16_t *p, int i) { return __uint_as_float((uint32_t)p[i] << 16); }
 __device__ __forceinline__ float one_of(const float *p, int i) { return p[i]; }
-
-// Numbers that order as the logits do (the zeros alike), and back.
-__device__ __forceinline__ uint32_t key_of(float l)
-{
-    const uint32_t b = __float_as_uint(l + 0.0f);
-    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float logit_of(uint32_t k)
-{
-    return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
-}
-
-// The bins of a row, counted downwards from the one of its largest logit.
-struct Scale {
-    double c1, c2, c3, c4;       // excess(f) = f (c1 + f (c2 + f (c3 + f c4))), f = place in the bin
-    double t;
-    float top, top_bin;          // largest logit, floor(top / d)
-    int shift;                   // d = 2^-shift
-    bool alone;                  // only tokens at `top` have a weight (top = +inf, or so far above T that its neighbours have none)
-    bool flat;                   // T = +inf: every token has weight one
-
-    __device__ __forceinline__ void set(float temperature, float largest)
-    {
-        top = largest;
-        t = temperature;
-        flat = temperature == INFINITY;
-        int e;
-        frexp(t, &e);                             // T in [2^(e-1), 2^e)
-        shift = flat ? -2000 : 6 - e;             // d = 2^(e-6): T / 64 < d <= T / 32
-        // from 2^36 d on the next smaller logits are 2048 bins away
-        alone = largest == INFINITY || fabs(ldexp((double)largest, shift)) >= 0x1p36;
-        top_bin = floorf(ldexpf(largest, shift));
-        // exp(x) - 1 for 0 <= x <= 1/32, as x times a polynomial through its four Chebyshev points: within 2^-38
-        const double w = flat ? 0.0 : ldexp(1.0, -shift) / t;
-        c1 = w * 0x1.ffffffff76092p-1 * kOne;
-        c2 = w * w * 0x1.00000227c482ap-1 * kOne;
-        c3 = w * w * w * 0x1.554ff31ff6e04p-3 * kOne;
-        c4 = w * w * w * w * 0x1.59a176b303773p-5 * kOne;
-    }
-    // Bin of l as a number, at least kBins or NaN where it has none (l NaN or -inf).
-    __device__ __forceinline__ float bin(float l) const
-    {
-        if (alone)
-            return l == top ? 0.0f : INFINITY;
-        return top_bin - floorf(ldexpf(l, shift));
-    }
-    // The excess of the logit a / to_bin in the low 47 bits of a double, and a count
-    // of one above it: the sum 2^52 + 2^47 + excess is whole, so its bits are those
-    // numbers under the exponent's.
-    __device__ __forceinline__ uint64_t raw_excess(float a) const
-    {
-        const double f = __builtin_amdgcn_fract((double)a);
-        return (uint64_t)__double_as_longlong(fma(f, fma(f, fma(f, fma(f, c4, c3), c2), c1), 0x1p52 + 0x1p47));
-    }
-    __device__ __forceinline__ uint64_t weight(float l) const
-    {
-        return (uint64_t)kOne + (alone ? 0 : raw_excess(ldexpf(l, shift)) & kExcess);
-    }
-    // lower edge of a bin, as a logit, and its weight relative to the largest logit
-    __device__ __forceinline__ double edge(int b) const { return ldexp((double)top_bin - b, -shift); }
-    __device__ __forceinline__ double edge_weight(int b) const
-    {
-        return alone || flat ? 1.0 : exp((edge(b) - (double)top) / t);
-    }
-};
 
 __device__ __forceinline__ bool greedy(float t) { return !(t > 0.0f); }
 
@@ -432,25 +364,6 @@ struct Draw {
     }
     __device__ __forceinline__ uint32_t *picked() const { return reinterpret_cast<uint32_t *>(upto); }
 
-    // Logits that the bins lo .. hi hold.
-    __device__ __forceinline__ void span(int lo, int hi, float &from, float &to) const
-    {
-        if (s.alone) {
-            from = to = s.top;
-            return;
-        }
-        from = -__FLT_MAX__;
-        to = s.top;
-        if (s.flat)
-            return;
-        // the first logit from the lower edge on, the last one in front of the upper one
-        const double e0 = s.edge(hi), e1 = s.edge(lo - 1);
-        const float f0 = (float)e0, f1 = (float)e1;
-        from = fmaxf((double)f0 < e0 ? logit_of(key_of(f0) + 1) : f0, from);
-        if (lo > 0)
-            to = fminf((double)f1 >= e1 ? logit_of(key_of(f1) - 1) : f1, to);
-    }
-
     // Puts the list's n entries in order and adds their weights up.  Where an entry
     // will stand is guessed from its place in its bin (r: the list's bins; none: all
     // entries are of one bin, with keys from klo to khi); entries of one guess count
@@ -489,14 +402,7 @@ struct Draw {
                         const uint32_t held = sh.cpre[b + 1] - sh.cpre[b];
                         for (int q = 0; q < r->n; ++q)
                             at[i] += sh.cpre[min(max(b, r->lo[q]), r->hi[q] + 1)] - sh.cpre[r->lo[q]];
-                        // equal logits of 16 bits, of which a bin holds few different ones, are spread by their
-                        // index over the step below the next larger logit; of one weight for all (flat) the bin
-                        // says nothing of a logit's place
-                        const int step = (int)(__float_as_uint(l) >> 23 & 255) - 134 + s.shift;
-                        const float u = s.flat ? 0.0f : s.alone ? 1.0f : sizeof(T) == 2 ? fminf(ldexpf(1.0f, step), 1.0f) : 0.0f;
-                        const float f = s.flat ? 1.0f : s.alone ? 0.0f : __builtin_amdgcn_fractf(ldexpf(l, s.shift));
-                        const float below = 1.0f - f - u + u * (float)(uint32_t)e[i] / (float)a.vocab;
-                        at[i] += min((uint32_t)(fmaxf(below, 0.0f) * (float)held), held - 1);
+                        at[i] += s.guess(l, sizeof(T) == 2, (uint32_t)e[i], a.vocab, held);
                     } else {
                         at[i] = (uint32_t)(((uint64_t)(khi - key) * (uint32_t)n) / ((uint64_t)(khi - klo) + 1));
                     }
@@ -564,7 +470,7 @@ struct Draw {
     __device__ Found search(int b, uint32_t n, Query q)
     {
         float from, to;
-        span(b, b, from, to);
+        s.span(b, b, from, to);
         uint32_t klo = key_of(from), khi = key_of(to);
         uint32_t count0 = 0;         // tokens and weight of the bin in front of [klo, khi]
         uint64_t weight0 = 0;
@@ -872,7 +778,7 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         if (lane < n) {
             r.lo[lane] = mine_lo;
             r.hi[lane] = mine_hi;
-            d.span(mine_lo, mine_hi, r.from[lane], r.to[lane]);
+            s.span(mine_lo, mine_hi, r.from[lane], r.to[lane]);
         }
         if (read == 1 && lane == n - 1)
             r.from[0] = r.from[n - 1];
@@ -934,7 +840,7 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
     }
     if (!gathered && least_lo < kBins) {
         float lo, hi;
-        d.span(least_lo, sh.least_hi, lo, hi);
+        s.span(least_lo, sh.least_hi, lo, hi);
         d.each(lo, hi, [&](int, float x) {
             if (s.bin(x) <= (float)sh.least_hi && heavy(x))
                 atomicAdd(&sh.passed, 1u);
