@@ -557,7 +557,7 @@ struct Draw {
                 list[min(atomicAdd(&sh.n, 1u), (uint32_t)kList - 1)] = (uint64_t)~key_of(x) << 32 | (uint32_t)at;
         });
         __syncthreads();
-        order((int)n, nullptr, klo, khi);
+        order((int)min(sh.n, (uint32_t)kList), nullptr, klo, khi);
         const Found f = among(0, (int)n, count0, weight0, q);
         __syncthreads();
         return f;
@@ -836,7 +836,7 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         }
         __syncthreads();
         if (gathered)
-            d.order((int)listed, &r, 0, 0);
+            d.order((int)min(sh.n, (uint32_t)kList), &r, 0, 0);
     }
     if (!gathered && least_lo < kBins) {
         float lo, hi;

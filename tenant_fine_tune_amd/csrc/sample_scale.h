@@ -78,7 +78,7 @@ struct Scale {
     {
         return alone || flat ? 1.0 : exp((edge(b) - (double)top) / t);
     }
-    // Logits that the bins lo .. hi hold.
+    // Logits between which the bins' lo .. hi lie; bin() says of those at an end in which they are.
     __host__ __device__ __forceinline__ void span(int lo, int hi, float &from, float &to) const
     {
         if (alone) {
@@ -93,6 +93,9 @@ struct Scale {
         const double e0 = edge(hi), e1 = edge(lo - 1);
         const float f0 = (float)e0, f1 = (float)e1;
         from = fmaxf((double)f0 < e0 ? logit_of(key_of(f0) + 1) : f0, from);
+        // negative logits that scale to less than half the smallest number are in the bin from zero on
+        if (e0 == 0.0)
+            from = -ldexpf(1.0f, -150 - shift);
         if (lo > 0)
             to = fminf((double)f1 >= e1 ? logit_of(key_of(f1) - 1) : f1, to);
     }

@@ -84,10 +84,35 @@ static void check_guesses(const std::vector<float> &v, bool sixteen)
     }
 }
 
+// Every logit that is counted in a bin is among those that the bin's span names, as
+// that of a range of bins too.
+static void check_spans(const std::vector<float> &v)
+{
+    for (float t : kTemperatures) {
+        Scale s;
+        for (size_t i = 0; i < v.size(); ++i)
+            for (size_t above : {(size_t)0, (size_t)1, (size_t)7, v.size() / 100, v.size() / 2}) {
+                s.set(t, v[std::min(i + above, v.size() - 1)]);
+                const float b = s.bin(v[i]);
+                if (!(b < kBins))
+                    continue;
+                EXPECT(b >= 0, "T=%g: %.9g, largest %.9g: bin %g", t, v[i], s.top, b);
+                for (int lo : {0, 1, 0x10000})
+                    for (int hi : {0, 3}) {
+                        float from, to;
+                        s.span(std::max((int)b - lo, 0), std::min((int)b + hi, kBins - 1), from, to);
+                        EXPECT(v[i] >= from && v[i] <= to, "T=%g: %.9g, largest %.9g: bin %g holds %.9g to %.9g", t, v[i], s.top, b, from, to);
+                    }
+            }
+    }
+}
+
 int main()
 {
     check_guesses(bf16_numbers(), true);
     check_guesses(f32_numbers(), false);
+    check_spans(bf16_numbers());
+    check_spans(f32_numbers());
     printf("sample scale: %d failures\n", failures);
     return failures != 0;
 }

@@ -62,3 +62,18 @@ def test_the_last_kept_token_of_a_full_bin(bd, border, dtype):
         rows = on.expand(len(at), n).contiguous()
         last, _ = bd.sample(rows, torch.ones(len(at), device=DEV), top_k=at.int().to(DEV))
         assert int((last.cpu().long() != order[at - 1]).sum()) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t,size", [(64.0, 2.0 ** -140), (100.0, 2.0 ** -146), (1e10, 1e-38), (1e20, 1e-25), (3e38, 1e-9), (3e38, 1e-20)])
+@pytest.mark.parametrize("n", [60, 1000, 6000])
+def test_logits_next_to_zero_at_high_temperatures(bd, n, t, size, dtype):
+    """Negative logits that scale to nothing share a bin with zero; all weigh the same, so every border is at a whole number."""
+    g = torch.Generator().manual_seed(5)
+    l = ((torch.rand(n, generator=g, dtype=torch.float64) * 2 - 1.5) * size).to(dtype)
+    l[torch.randperm(n, generator=g)[:n // 5]] = 0.0
+    l[torch.randperm(n, generator=g)[:n // 9]] = -0.0
+    every_place(bd, l, t, 1000)
+    # beside logits of ordinary size: only some of the candidates are next to zero
+    l[::3] = torch.randn(len(l[::3]), generator=g).to(dtype)
+    every_place(bd, l, t, 1000)
