@@ -310,7 +310,7 @@ struct Draw {
     uint64_t *list, *upto;               // ~key and index of tokens, in order once order() was called; their weights added up
     Scale s;
 
-    // Calls f(token, logit) for every token whose logit is within [lo, hi].
+    // Calls f(token, logit) for every token whose logit is in [lo, hi].
     template <typename F>
     __device__ __forceinline__ void each(float lo, float hi, F f)
     {
@@ -487,7 +487,7 @@ struct Draw {
                 counts[i] = 0, sums[i] = 0;
             __syncthreads();
             each(logit_of(klo), logit_of(khi), [&](int, float x) {
-                if (s.bin(x) == b) {
+                if (within(x, klo, khi) && s.bin(x) == b) {
                     const uint32_t i = (khi - key_of(x)) >> shift;
                     atomicAdd(&counts[i], 1u);
                     atomicAdd((unsigned long long *)&sums[i], (unsigned long long)s.weight(x));
@@ -553,7 +553,7 @@ struct Draw {
             sh.n = 0;
         __syncthreads();
         each(logit_of(klo), logit_of(khi), [&](int at, float x) {
-            if (s.bin(x) == b)
+            if (within(x, klo, khi) && s.bin(x) == b)
                 list[min(atomicAdd(&sh.n, 1u), (uint32_t)kList - 1)] = (uint64_t)~key_of(x) << 32 | (uint32_t)at;
         });
         __syncthreads();

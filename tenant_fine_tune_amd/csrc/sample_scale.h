@@ -25,6 +25,12 @@ __host__ __device__ __forceinline__ float logit_of(uint32_t k)
 {
     return __builtin_bit_cast(float, k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
 }
+// Whether l's number is one of lo .. hi.  Compared as logits the zeros would be in the
+// range below theirs too, whose last number stands for the negative zero.
+__host__ __device__ __forceinline__ bool within(float l, uint32_t lo, uint32_t hi)
+{
+    return key_of(l) - lo <= hi - lo;
+}
 
 // The bins of a row, counted downwards from the one of its largest logit.
 struct Scale {

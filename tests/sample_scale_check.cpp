@@ -107,12 +107,24 @@ static void check_spans(const std::vector<float> &v)
     }
 }
 
+// Of two neighbouring ranges of keys a logit is in one, wherever they meet.
+static void check_ranges(const std::vector<float> &v)
+{
+    for (size_t i = 0; i < v.size(); ++i) {
+        const uint32_t key = key_of(v[i]);
+        EXPECT(logit_of(key) == v[i], "%.9g", v[i]);
+        for (uint32_t meet : {key - 3, key - 1, key, key + 1, 0x7FFFFFFEu, 0x7FFFFFFFu, 0x80000000u})
+            EXPECT(within(v[i], key_of(-__FLT_MAX__), meet) != within(v[i], meet + 1, key_of(INFINITY)), "%.9g, ranges meet at %08x", v[i], meet);
+    }
+}
+
 int main()
 {
     check_guesses(bf16_numbers(), true);
     check_guesses(f32_numbers(), false);
     check_spans(bf16_numbers());
     check_spans(f32_numbers());
+    check_ranges(f32_numbers());
     printf("sample scale: %d failures\n", failures);
     return failures != 0;
 }

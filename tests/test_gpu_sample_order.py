@@ -77,3 +77,15 @@ def test_logits_next_to_zero_at_high_temperatures(bd, n, t, size, dtype):
     # beside logits of ordinary size: only some of the candidates are next to zero
     l[::3] = torch.randn(len(l[::3]), generator=g).to(dtype)
     every_place(bd, l, t, 1000)
+
+
+@pytest.mark.parametrize("rows", [200, 1000])
+def test_ranges_that_meet_at_zero(bd, rows):
+    """All tokens alike and too many for one list: smaller ranges of logits, one of which ends right below zero
+    (they are cut from the largest logit down, by 2^21 numbers)."""
+    g = torch.Generator().manual_seed(6)
+    n = 7000
+    l = torch.cat([torch.zeros(1500), -torch.zeros(1500), (torch.randperm(2 ** 20, generator=g)[:n - 3001] + 1) * -(2.0 ** -149),
+                   torch.tensor([1.25 - 2.0 ** -23])])[torch.randperm(n, generator=g)]
+    assert int(l.max().view(torch.int32)) & 0x1FFFFF == 0x1FFFFF and len(l.unique()) == n - 3001 + 2
+    every_place(bd, l, float("inf"), rows)
