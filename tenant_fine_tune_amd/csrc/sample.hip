@@ -671,10 +671,11 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
     };
 
     // Which bins hold a border, and between what the kept weight lies.
-    const int32_t k = a.top_k ? a.top_k[row] : a.top_k_all;
     const float p = a.top_p ? a.top_p[row] : a.top_p_all;
-    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all, least = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
-    const bool by_k = k > 0 && (uint32_t)k < all, by_p = p < 1.0f, by_least = least > 0.0f && !s.alone && !s.flat;
+    const float least = a.min_p ? a.min_p[row] : a.min_p_all;
+    // no token weighs more than one: a limit above that leaves the first alone
+    const int32_t k = least > 1.0f ? 1 : a.top_k ? a.top_k[row] : a.top_k_all;
+    const bool by_k = k > 0 && (uint32_t)k < all, by_p = p < 1.0f, by_least = least > 0.0f && least <= 1.0f && !s.alone && !s.flat;
     constexpr double kLess = 1.0 - 0x1p-45, kMore = 1.0 + 0x1p-45;     // roundings of the sums
     const float u = a.u[row] > 0.0f ? a.u[row] : 0.0f;
     // below the kept weight whatever u

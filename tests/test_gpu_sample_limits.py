@@ -1,0 +1,41 @@
+"""GPU tier: limits of the draw where tokens are alike."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def bd():
+    import tenant_fine_tune_amd as bd
+
+    return bd
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("min_p", [1.0 + 2.0 ** -23, 1.5, 3e38, math.inf])
+@pytest.mark.parametrize("t", [0.7, 1.0, 1e20, math.inf])
+@pytest.mark.parametrize("top", [2.0, -3.0, 1e30, math.inf])
+def test_min_p_above_one_keeps_the_first_token(bd, top, t, min_p, dtype):
+    """No weight reaches it, and the first token is always kept: the lowest index of equal largest logits."""
+    g = torch.Generator().manual_seed(1)
+    l = torch.randn(12, 5000, generator=g) - 9.0
+    first = torch.empty(12, dtype=torch.long)
+    for i in range(12):
+        at = torch.randperm(5000, generator=g)[:1 + 300 * i]
+        l[i, at] = top
+        first[i] = at.min()
+    l = l.to(dtype).to(DEV)
+    u = torch.linspace(0.0, 1.0, 12, device=DEV)
+    for value in (min_p, torch.full((12,), min_p, device=DEV)):
+        for more in (dict(), dict(top_k=7), dict(top_p=0.9)):
+            tokens, logprobs = bd.sample(l, u, temperature=t, min_p=value, **more)
+            assert torch.equal(tokens.cpu().long(), first) and (logprobs == 0).all()
+    # one is a weight that the equal ones reach
+    tokens, _ = bd.sample(l, torch.ones(12, device=DEV), temperature=t, min_p=1.0)
+    ties = l == l.max(1, keepdim=True).values
+    if t < 1e20:
+        assert torch.equal(tokens.cpu().long(), 4999 - ties.flip(1).int().argmax(1).cpu())
