@@ -368,7 +368,7 @@ struct Draw {
     // will stand is guessed from its place in its bin (r: the list's bins; none: all
     // entries are of one bin, with keys from klo to khi); entries of one guess count
     // those before them among themselves.
-    __device__ void order(int n, const Ranges *r, uint32_t klo, uint32_t khi)
+    __device__ __forceinline__ void order(int n, const Ranges *r, uint32_t klo, uint32_t khi)
     {
         if (n <= kFew) {
             uint64_t e = 0;
