@@ -225,25 +225,45 @@ __device__ __forceinline__ V wave_scan(V v)
     return v;
 }
 
-// Sum of v over the threads before this one; `total` over all of them.
+// Number i of a thread's N stands at place i * TH + its own: their sums over the places in
+// front, `total` over all of them.
+template <int TH, int N, typename V>
+__device__ __forceinline__ void scan(const V (&v)[N], V *part, V (&before)[N], V &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    V s[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        s[i] = wave_scan(v[i]);
+    __syncthreads();          // part may still be read from the scan before
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (lane == 63)
+            part[i * (TH / 64) + wave] = s[i];
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        before[i] = 0;
+#pragma unroll
+    for (int w = 0; w < N * (TH / 64); ++w) {
+        const V x = part[w];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            before[i] += w < i * (TH / 64) + wave ? x : V(0);
+        total += x;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        before[i] += moved<kWave1>(s[i], V(0));
+}
 template <int TH, typename V>
 __device__ __forceinline__ V scan(V v, V *part, V &total)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const V s = wave_scan(v);
-    __syncthreads();          // part may still be read from the scan before
-    if (lane == 63)
-        part[wave] = s;
-    __syncthreads();
-    V before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < TH / 64; ++w) {
-        const V x = part[w];
-        before += w < wave ? x : V(0);
-        total += x;
-    }
-    return before + moved<kWave1>(s, V(0));
+    const V mine[1] = {v};
+    V before[1];
+    scan<TH>(mine, part, before, total);
+    return before[0];
 }
 
 // The first of n <= 4096 places that is right, n - 1 if no other is: `right` turns
@@ -290,9 +310,9 @@ struct Draw {
         uint64_t work[2 * kList];        // the list and its sums; smaller bins
         double wpre[kBins + 1];          // weights and tokens in front of a bin
         uint32_t cpre[kBins + 1];
-        double part_d[TH / 64];
+        double part_d[kBins / 128];
         unsigned long long part_u[TH / 64];
-        uint32_t part_c[TH / 64];
+        uint32_t part_c[kBins / 128];
         uint32_t guess[kList / 2];       // two 16-bit numbers each
         uint32_t n, passed;
         int32_t hit;
@@ -600,9 +620,11 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
     Scale &s = d.s;
     s.set(t, top);
 
-    // the row's bins, and the sums of counts and weights in front of them
-    constexpr int per = kBins / TH;
-    const int b0 = threadIdx.x * per;
+    // The row's bins, and the sums of counts and weights in front of them.  Two bins of a pair are
+    // added up first and the pairs stand as the places of 1024 threads do, however many there
+    // are: the weights' sums, which are rounded, are the same ones.
+    constexpr int per = kBins / TH, kPairs = per / 2;
+    auto bin_at = [&](int i) { return ((i >> 1) * TH + (int)threadIdx.x) * 2 + (i & 1); };
     uint64_t count[per], excess[per];
 #pragma unroll
     for (int i = 0; i < per; ++i)
@@ -619,8 +641,8 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
 #pragma unroll
             for (int i = 0; i < per; ++i) {
                 v[q][i] = 0;
-                if (first[q] <= (float)(b0 + i))
-                    v[q][i] = parts[p + q].bins[b0 + i - (int)first[q]];
+                if (first[q] <= (float)bin_at(i))
+                    v[q][i] = parts[p + q].bins[bin_at(i) - (int)first[q]];
             }
 #pragma unroll
         for (int q = 0; q < kTogether; ++q)
@@ -630,27 +652,32 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
                 excess[i] += v[q][i] & kExcess;
             }
     }
-    uint32_t counts = 0, all;
-    double weight[per], weights = 0, total;
+    uint32_t counts[kPairs], cs[kPairs], all;
+    double weight[per], weights[kPairs], ws[kPairs], total;
 #pragma unroll
     for (int i = 0; i < per; ++i) {
+#pragma clang fp contract(off)
         const uint64_t w = count[i] * (uint64_t)kOne + excess[i];
-        weight[i] = w ? (double)w * (1.0 / kOne) * s.edge_weight(b0 + i) : 0.0;
-        counts += (uint32_t)count[i];
-        weights += weight[i];
+        weight[i] = w ? (double)w * (1.0 / kOne) * s.edge_weight(bin_at(i)) : 0.0;
     }
-    uint32_t cs = scan<TH>(counts, sh.part_c, all);
-    double ws = scan<TH>(weights, sh.part_d, total);
 #pragma unroll
-    for (int i = 0; i < per; ++i) {
-        sh.cpre[b0 + i] = cs;
-        sh.wpre[b0 + i] = ws;
-        cs += (uint32_t)count[i];
-        ws += weight[i];
+    for (int i = 0; i < kPairs; ++i) {
+        counts[i] = (uint32_t)count[2 * i] + (uint32_t)count[2 * i + 1];
+        weights[i] = weight[2 * i] + weight[2 * i + 1];
+    }
+    scan<TH>(counts, sh.part_c, cs, all);
+    scan<TH>(weights, sh.part_d, ws, total);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const int b = bin_at(2 * i);
+        sh.cpre[b] = cs[i];
+        sh.wpre[b] = ws[i];
+        sh.cpre[b + 1] = cs[i] + (uint32_t)count[2 * i];
+        sh.wpre[b + 1] = ws[i] + weight[2 * i];
     }
     if (threadIdx.x == TH - 1) {
-        sh.cpre[kBins] = cs;
-        sh.wpre[kBins] = ws;
+        sh.cpre[kBins] = cs[kPairs - 1] + counts[kPairs - 1];
+        sh.wpre[kBins] = ws[kPairs - 1] + weight[per - 2] + weight[per - 1];
     }
     if (threadIdx.x == 0)
         sh.n = sh.passed = 0;
