@@ -942,6 +942,15 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         } else {
             kept = cap.weight;
             w = target(kept);
+            if (u >= 1.0f) {
+                // the last kept token, which may weigh less than a rounding of the sums
+                if (cap.bin < kBins && cap.f.weight != ~0ull) {
+                    entry = cap.f.entry;
+                    continue;
+                }
+                c = sh.cpre[min(cap.bin, kBins - 1) + 1];
+                w = 0.0;
+            }
         }
         const Border e = border(stage == 2 ? 3 : min(stage, 2), c, w, stage == 3);
         if (stage == 3)
