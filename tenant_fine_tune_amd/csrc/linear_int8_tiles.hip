@@ -53,8 +53,8 @@ __device__ __forceinline__ uint32_t signed_bytes(uint32_t w, int at)
 }
 
 // A call over rows of whole 32 columns: as given, or with the tokens' numbers and
-// the signs in copies that zeros fill up, while w keeps its own stride.  What the
-// tiles then read of w past a row's end meets zeros.
+// the signs in copies that zeros fill up, while w keeps its own stride (how its rows'
+// ends are read and copied: int8_tiles.h).
 struct TileArgs : Int8Args {
     int64_t w_stride;
 };
@@ -125,10 +125,12 @@ void int8_tiles(TileArgs a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int s
     // copy i of this wave covers 8 rows; lane l writes place l & 7 of row l / 8.
     // Rows that do not exist have an offset out of range (zeros); the step's
     // columns go into the scalar offset, which is not checked, so the last step's
-    // lanes past the row's end have theirs out of range too.
+    // lanes past the row's end have theirs out of range too, and w's have the whole of
+    // their place in it.
     const int place = lane & 7;
-    uint32_t xoff[XI], woff[WI], soff[SI ? SI : 1];
-    int xk[XI], wk[WI];
+    const int steps = (int)((K + kStep - 1) / kStep), begin = (int)((int64_t)steps * split / splits);
+    uint32_t xoff[XI], woff[WI], wlast[WI], soff[SI ? SI : 1];
+    int xk[XI];
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
         const int row = (wave * XI + i) * 8 + (lane >> 3);
@@ -138,26 +140,27 @@ void int8_tiles(TileArgs a, int64_t m_tiles, int64_t n_tiles, bool n_fast, int s
 #pragma unroll
     for (int i = 0; i < WI; ++i) {
         const int row = (wave * WI + i) * 8 + (lane >> 3);
-        wk[i] = (place ^ ((row >> 1) & 7)) * 16;
-        woff[i] = n0 + row < N ? (uint32_t)((n0 + row) * a.w_stride + wk[i]) : kInvalidOffset;
+        const int wk = (place ^ ((row >> 1) & 7)) * 16, column = chunk_column((steps - 1) * kStep + wk, (int)a.w_stride);
+        woff[i] = n0 + row < N ? (uint32_t)((n0 + row) * a.w_stride + wk) : kInvalidOffset;
+        wlast[i] = n0 + row < N && column >= 0 ? (uint32_t)((n0 + row) * a.w_stride + column) : kInvalidOffset;
     }
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
         const int row = (wave * SI + i) * 16 + (lane >> 2);
         soff[i] = n0 + row < N ? (uint32_t)((n0 + row) * G + (lane & 3) * 4) : kInvalidOffset;
     }
-    const int steps = (int)((K + kStep - 1) / kStep), begin = (int)((int64_t)steps * split / splits);
     const int T = (int)((int64_t)steps * (split + 1) / splits) - begin;
     const int last = (int)(K - (int64_t)(steps - 1) * kStep);     // columns of the last step
     auto copy = [&](int t, int buf) {
         const uint32_t k = (uint32_t)(begin + t) * kStep;
-        const int have = begin + t == steps - 1 ? last : kStep;
+        const bool end = begin + t == steps - 1;
+        const int have = end ? last : kStep;
 #pragma unroll
         for (int i = 0; i < XI; ++i)
             copy16(rx, xs[buf] + (wave * XI + i) * 1024, xk[i] < have ? xoff[i] : kInvalidOffset, k);
 #pragma unroll
         for (int i = 0; i < WI; ++i)
-            copy16(rw, ws[buf] + (wave * WI + i) * 1024, wk[i] < have ? woff[i] : kInvalidOffset, k);
+            copy16(rw, ws[buf] + (wave * WI + i) * 1024, end ? wlast[i] : woff[i], end ? 0 : k);
 #pragma unroll
         for (int i = 0; i < SI; ++i)
             copy4(rs, ss[buf] + (wave * SI + i) * 256, (lane & 3) * 32 < have ? soff[i] : kInvalidOffset, k / 8);
@@ -334,8 +337,9 @@ __global__ __launch_bounds__(256) void int8_pad(const uint64_t *__restrict__ q, 
 {
     uint32_t i = blockIdx.x * 256 + threadIdx.x;
     if (i < q_units) {
-        const uint32_t row = i / padded, at = i % padded;
-        q_to[i] = at < G ? q[row * G + at] : 0;
+        const uint32_t row = i / padded;
+        const int from = copied_group(i % padded, G);
+        q_to[i] = from >= 0 ? q[row * G + from] : 0;
         return;
     }
     i -= q_units;
@@ -343,9 +347,11 @@ __global__ __launch_bounds__(256) void int8_pad(const uint64_t *__restrict__ q, 
         return;
     const uint32_t row = i / (padded / 4), at = i % (padded / 4) * 4;
     uint32_t w = 0;
-    for (uint32_t b = 0; b < 4; ++b)
-        if (at + b < G)
-            w |= (uint32_t)signs[(uint64_t)row * G + at + b] << (8 * b);
+    for (uint32_t b = 0; b < 4; ++b) {
+        const int from = copied_group(at + b, G);
+        if (from >= 0)
+            w |= (uint32_t)signs[(uint64_t)row * G + from] << (8 * b);
+    }
     signs_to[i] = w;
 }
 
@@ -462,13 +468,14 @@ size_t sums_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 // Whether rows that end inside 32 columns are copied for the tiles: the copy of all
 // variants' signs has to be paid for by the tokens (333 tokens of 3 variants through
 // 1000 x 4104: by the kernel for 64 tokens 60 us, copied 33), and stays below 2^28 bytes.
+// A row of 8 columns is less than a chunk, which so would begin in front of w.
 size_t pad_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
     return (size_t)(m * whole(d_in) + n_variants * (d_out * (whole(d_in) / 8)) + 31) / 16 * 16;
 }
 bool pads(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
-    return d_in % 32 != 0 && n_variants <= m / 4 && pad_bytes(m, n_variants, d_out, d_in) <= (size_t)1 << 28;
+    return d_in % 32 != 0 && d_in > 8 && n_variants <= m / 4 && pad_bytes(m, n_variants, d_out, d_in) <= (size_t)1 << 28;
 }
 
 }  // namespace
