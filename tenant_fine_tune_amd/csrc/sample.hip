@@ -800,8 +800,7 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         const uint32_t upto = wave_scan(lane < n ? past - first : 0u);
         const uint32_t listed = (uint32_t)__builtin_amdgcn_readlane((int)upto, 3);
         const uint32_t all_of = (uint32_t)__builtin_amdgcn_readlane((int)past, n - 1) - (uint32_t)__builtin_amdgcn_readlane((int)first, 0);
-        // each range costs a comparison with every logit, a token read in vain some more: one range where few lie between
-        const int read = n > 1 && all_of - listed <= (uint32_t)a.vocab / 64 ? 1 : n;
+        const int read = ranges_read(n, listed, all_of, a.vocab, Draw<TH, T>::kPicked);
         Ranges &r = sh.r;
         if (lane < n) {
             r.lo[lane] = mine_lo;

@@ -32,6 +32,14 @@ __host__ __device__ __forceinline__ bool within(float l, uint32_t lo, uint32_t h
     return key_of(l) - lo <= hi - lo;
 }
 
+// How many ranges n ranges of candidates are read as.  Each costs a comparison with every
+// logit, a token read in vain some more: one where few lie between, as long as all
+// that it holds find room.
+__host__ __device__ __forceinline__ int ranges_read(int n, uint32_t listed, uint32_t in_one, int32_t vocab, uint32_t room)
+{
+    return n > 1 && in_one - listed <= (uint32_t)vocab / 64 && in_one <= room ? 1 : n;
+}
+
 // The bins of a row, counted downwards from the one of its largest logit.
 struct Scale {
     double c1, c2, c3, c4;       // excess(f) = f (c1 + f (c2 + f (c3 + f c4))), f = place in the bin

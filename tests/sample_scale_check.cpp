@@ -118,6 +118,20 @@ static void check_ranges(const std::vector<float> &v)
     }
 }
 
+// Ranges read as one find room, as they do one by one.
+static void check_reading()
+{
+    for (uint32_t room : {5120u, 8192u})
+        for (int32_t vocab : {2, 1000, 131071, 262144, 300000, 1048576})
+            for (uint32_t listed : {2u, 100u, room / 2})
+                for (uint32_t between : {0u, 100u, (uint32_t)vocab / 64, (uint32_t)vocab / 64 + 1, room / 2, room / 2 + 1, room})
+                    for (int n : {1, 2, 4}) {
+                        const int r = ranges_read(n, listed, listed + between, vocab, room);
+                        EXPECT(r == n || (r == 1 && listed + between <= room), "%d ranges, %u and %u between, %d logits", n, listed, between, vocab);
+                        EXPECT(n == 1 || between > 100 || vocab < 6400 || r == 1, "%d ranges, %u between, %d logits", n, between, vocab);
+                    }
+}
+
 int main()
 {
     check_guesses(bf16_numbers(), true);
@@ -125,6 +139,7 @@ int main()
     check_spans(bf16_numbers());
     check_spans(f32_numbers());
     check_ranges(f32_numbers());
+    check_reading();
     printf("sample scale: %d failures\n", failures);
     return failures != 0;
 }

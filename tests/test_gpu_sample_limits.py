@@ -39,3 +39,16 @@ def test_min_p_above_one_keeps_the_first_token(bd, top, t, min_p, dtype):
     ties = l == l.max(1, keepdim=True).values
     if t < 1e20:
         assert torch.equal(tokens.cpu().long(), 4999 - ties.flip(1).int().argmax(1).cpu())
+
+
+@pytest.mark.parametrize("k", [4000, 9000, 14000, 30000])
+@pytest.mark.parametrize("u", [0.01, 0.2])
+def test_distant_borders_of_a_million_logits(bd, k, u):
+    """The candidates of the last kept token and of the drawn one, and as many or more tokens between them."""
+    from tests import sample_ref
+
+    g = torch.Generator().manual_seed(2)
+    l = torch.randn(3, 1048576, generator=g) * 2
+    uu, one = torch.full((3,), u) + torch.arange(3) * 0.003, torch.ones(3)
+    tokens, logprobs = bd.sample(l.to(DEV), uu.to(DEV), top_k=k, min_p=1e-4)
+    sample_ref.check(tokens, logprobs, l, uu, one, (one * k).int(), one, torch.full((3,), 1e-4))
