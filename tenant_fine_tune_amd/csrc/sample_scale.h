@@ -111,7 +111,7 @@ struct Scale {
         if (e0 == 0.0)
             from = -ldexpf(1.0f, -150 - shift);
         if (lo > 0)
-            to = fminf((double)f1 >= e1 ? logit_of(key_of(f1) - 1) : f1, to);
+            to = fminf((double)f1 >= e1 ? logit_of(key_of(f1) - (f1 == 0.0f ? 2 : 1)) : f1, to);     // in front of zero: its negative is none
     }
     // About where a token of a bin that holds `held` stands among those, in their order: a
     // guess that puts none in front of one that comes before it.  Equal logits of 16

@@ -132,6 +132,21 @@ static void check_reading()
                     }
 }
 
+// The bin that ends at zero does not name the zeros, of which a row may have any number.
+static void check_below_zero()
+{
+    for (float t : kTemperatures) {
+        Scale s;
+        s.set(t, 3.0f * t);
+        if (s.alone || s.flat)
+            continue;
+        const int below = (int)s.bin(0.0f) + 1;
+        float from, to;
+        s.span(below, below, from, to);
+        EXPECT(to < 0.0f && (from < 0.0f || t < 1e-44f), "T=%g: bin %d holds %.9g to %.9g", t, below, from, to);
+    }
+}
+
 int main()
 {
     check_guesses(bf16_numbers(), true);
@@ -140,6 +155,7 @@ int main()
     check_spans(f32_numbers());
     check_ranges(f32_numbers());
     check_reading();
+    check_below_zero();
     printf("sample scale: %d failures\n", failures);
     return failures != 0;
 }

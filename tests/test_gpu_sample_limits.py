@@ -52,3 +52,22 @@ def test_distant_borders_of_a_million_logits(bd, k, u):
     uu, one = torch.full((3,), u) + torch.arange(3) * 0.003, torch.ones(3)
     tokens, logprobs = bd.sample(l.to(DEV), uu.to(DEV), top_k=k, min_p=1e-4)
     sample_ref.check(tokens, logprobs, l, uu, one, (one * k).int(), one, torch.full((3,), 1e-4))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [4, 300])
+def test_borders_in_front_of_many_zeros(bd, rows, dtype):
+    """A border among the tokens right below zero, with most of the row at zero."""
+    g = torch.Generator().manual_seed(3)
+    n, small = 120000, 300
+    l = torch.zeros(n)
+    l[::2] = -0.0
+    at = torch.randperm(n, generator=g)
+    l[at[:small]] = -torch.rand(small, generator=g) / 40 - 2.0 ** -20
+    l[at[small:2 * small]] = -1.0
+    l[at[-1]] = 2.0
+    l = l.to(dtype)
+    order = torch.sort(l.double(), descending=True, stable=True).indices
+    k = n - 2 * small + torch.linspace(1, small, rows).int()
+    tokens, _ = bd.sample(l.to(DEV).expand(rows, n).contiguous(), torch.ones(rows, device=DEV), top_k=k.to(DEV))
+    assert int((tokens.cpu().long() != order[k.long() - 1]).sum()) == 0
