@@ -142,8 +142,8 @@ __device__ __forceinline__ void finish(const Int8Args &a, int64_t t0, int count,
 // The tokens are ordered by variant; a variant's product is formed for all 16 and
 // kept for its own.
 // MANY: with variant ids.
-// One token through 8192 x 8192 with one delta 14.9 us, 5.1 TB/s; 16 of 14 variants
-// through 10240 x 8192 50 us, 3.6 TB/s, between the variants' 64-byte pieces of rows.
+// One token through 8192 x 8192 with one delta 15.7 us, 4.8 TB/s; 16 of 14 variants
+// through 10240 x 8192 50 us, 3.5 TB/s, between the variants' 64-byte pieces of rows.
 template <int NW, bool DELTA, bool MANY, Rows R>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4)))
 void int8_stream(Int8Args a)
@@ -338,9 +338,10 @@ void int8_stream(Int8Args a)
 // ranges, which share lines of signs, are read on one die at a time.  All waves
 // work on one range and share the tokens' numbers in LDS; the signs of the
 // following variants, the next range's among them, are on their way while one is used.
-// 32 tokens through 50257 x 8192 without a delta 93 us, 4.4 TB/s; 61 tokens of 14
-// variants through 8192 x 28672 209 us with the join, 3.0 TB/s: signs are spread to bytes
-// by vector instructions, two waves a SIMD hide little, and lines of signs are fetched twice.
+// 32 tokens through 50257 x 8192 without a delta 94 us, 4.4 TB/s; 61 tokens of 14
+// variants through 8192 x 28672 210 us with the join, 3.0 TB/s: signs are spread to bytes
+// by vector instructions (the waves' cycles: 41 % issue, 25 % wait to, 33 % wait for data),
+// two waves a SIMD hide little, and lines of signs are fetched twice (0.90 GB for 0.62).
 constexpr int kMidWaves = 4;
 
 template <int T, bool DELTA, bool MANY, Rows R>
@@ -591,12 +592,14 @@ __global__ __launch_bounds__(256) void int8_join(Int8Args a, int splits, const i
 
 // Splits of a call's columns: as many as give each CU two workgroups, of two ranges
 // at least, or one where each range meets many variants' signs.
-//   us, 64 tokens x 8192 columns, ranges at least    4      2      1   (with three loads of signs ahead)
-//     1024 channels, one delta                      18.3   16.0   18.6
-//                    4 variants                     36.1   27.1   26.0
-//                   14                              55.6   36.6   30.9
-//     2048 channels, none                           13.9   13.8   17.2
-//                   14                              57.3   39.9   38.0
+//   us, 64 tokens x 8192 columns, ranges at least    4      2      1
+//     1024 channels, none                           18.2   16.5   17.0
+//                    one delta                      20.1   17.6   18.7
+//                    4 variants                     31.3   26.0   26.4
+//                   14                              48.2   34.7   30.8
+//     2048 channels, none                           16.4   16.1   17.4
+//                    one delta                      21.0   20.3   22.7
+//                   14                              49.7   37.3   34.3
 template <int T>
 int mid_splits(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
@@ -655,14 +658,15 @@ hipError_t stream(const Int8Args &a, hipStream_t s)
 // Whether more than 64 tokens of many variants go in lots of 64: a tile has one
 // variant's tokens, few of its rows, and reads all of the base's for them, a lot
 // reads the base and its variants' signs once.
-//   us                        tiles   lots          tiles   lots
-//                             128 tokens            192 tokens
-//   8192 x 8192, 4 variants      71     72            104    108
-//               14              154    122            158    195
-//               38 of 64        334    186            366    305
-//   1024 x 8192, 14              37     35             43     43
-//   28672 x 8192, 14            422    408            456    555
-//               38 of 64       1023    673           1177    941
+//   us                        tiles   lots          tiles   lots          tiles   lots
+//                             128 tokens            192 tokens            256 tokens
+//   8192 x 8192, 4 variants      80     76            107    106             96    106
+//               14              154    113            158    173            159    191
+//               38              253    160            289    264            298    312
+//   1024 x 8192, 14              40     37             42     47             46     43
+//               38               59     41             68     57             73     55
+//   28672 x 8192, 14            420    413            437    579            454    688
+//               38              815    604            936    867            985   1103
 bool in_lots(const Int8Args &a)
 {
     const int64_t lots = (a.m + 63) / 64;
@@ -673,7 +677,7 @@ bool in_lots(const Int8Args &a)
 
 // Up to 16 tokens the waves of a workgroup share the columns, up to 64 they share
 // the tokens; from there on the tiles are used.  8192 x 8192, one delta: 16 tokens
-// 21 us, 24 tokens 23, 64 tokens 31, 65 tokens 33.
+// 21 us, 17 tokens 25, 64 tokens 33, 65 tokens 41 (the base from memory each time).
 constexpr int64_t kMidFrom = 17, kTilesFrom = 65;
 
 // Where the tiles do not take more than kSlice tokens they go by slices: a launch

@@ -12,8 +12,9 @@
 // two products need no common scale, nothing of W_eff is ever formed, and the
 // columns may be split over workgroups where the tiles are few.
 // Two or three workgroups a compute unit hide each other's waits.  2048 tokens
-// through 8192 x 8192 with one delta: four waves of 32 channels 262 us; four of 64
-// tokens x 64 channels 285; eight in a tile of 256 x 128 alone on its unit 300.
+// through 8192 x 8192 with one delta 270 us; where shapes were compared four waves of 32
+// channels took 262, four of 64 tokens x 64 channels 285, eight in a tile of 256 x 128
+// alone on its unit 300.
 //
 // In LDS the 16-byte chunk c of row r stands at c ^ ((r >> 1) & 7), so that the
 // reads of 32 rows spread over the banks.  One barrier a step.
@@ -393,6 +394,10 @@ size_t part_bytes(bool tall, int64_t m, int64_t d_out, int splits, bool delta, i
 //    1024                             166 (1)               140 (1)
 //   14 variants, 512                  184 (1)               234 (1)
 //                2048                 379 (1)               375 (1)
+// On 1024, 10240 and 28672 x 8192 and 8192 x 28672, with 128 to 2048 tokens, what this
+// picks takes at most 7 % longer than the best of both tiles and 1, 2, 4 or 8 splits, but
+// for 128 tokens through 1024 x 8192 (20 %), 2048 through 10240 x 8192 and 1024 through
+// 28672 x 8192 with one delta (13 and 10 %).
 Plan plan_of(int64_t m, int64_t d_out, int64_t d_in, bool delta, int32_t variants)
 {
     const int64_t steps = (d_in + kStep - 1) / kStep, n_tiles = (d_out + kBN - 1) / kBN;
@@ -468,7 +473,8 @@ size_t sums_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 // Whether rows that end inside 32 columns are copied for the tiles: the copy of all
 // variants' signs has to be paid for by the tokens (333 tokens of 3 variants through
 // 1000 x 4104: by the kernel for 64 tokens 60 us, copied 33), and stays below 2^28 bytes.
-// A row of 8 columns is less than a chunk, which so would begin in front of w.
+// A row of 8 columns is less than a chunk, which so would begin in front of w (4096 tokens
+// through 8192 x 8 192 us by the kernel for 64 tokens, rows of 16 columns 71).
 size_t pad_bytes(int64_t m, int32_t n_variants, int64_t d_out, int64_t d_in)
 {
     return (size_t)(m * whole(d_in) + n_variants * (d_out * (whole(d_in) / 8)) + 31) / 16 * 16;

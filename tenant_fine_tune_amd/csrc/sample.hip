@@ -24,7 +24,7 @@
 // sample_bins is bound by its vector instructions and LDS additions, one of 64 bits a
 // logit: 512 rows of 131071 bf16 logits 51 us (2.6 TB/s), one of 32000 4.2.  sample_draw
 // is bound by its stages, each waiting for the one before: one row 14 us, of which the
-// row's reading takes 2; 512 rows 52 to 56, of which 15 are the reading from the caches.
+// row's reading takes 2; 512 rows 52 to 57, of which 15 are the reading from the caches.
 #include "bd_device.h"
 #include "sample_launch.h"
 #include "sample_scale.h"
@@ -997,8 +997,9 @@ void start(const SampleArgs &a, Part *parts, hipStream_t s)
     default: sample_bins<1, T><<<grid, kBinThreads, 0, s>>>(a, parts, splits); break;
     }
     // up to a row a CU the wider form is faster; of more rows one is at its borders while another is read
-    // (512 rows of 131071 bf16 logits 106 us, by the wider form 114), as long as the shorter list holds the
-    // tokens of three full bins (three limits among the likely tokens, 300 rows of 220000: 308 us, 188 by the wider form)
+    // (512 rows of 131071 bf16 logits 103 us, by the wider form 113), as long as the shorter list holds the
+    // tokens of three full bins (264 rows of 250000, each with limits of its own: 258 us, 114 by the wider
+    // form; 400000: 532 and 301; where few tokens are at the borders the wider form takes 3 to 15 % longer)
     if (a.m <= 256 || a.vocab > 150000)
         sample_draw<1024, T><<<(unsigned)a.m, 1024, 0, s>>>(a, parts, splits);
     else
