@@ -869,7 +869,8 @@ void sample_draw(SampleArgs a, const Part *__restrict__ parts, int32_t splits)
         float lo, hi;
         s.span(least_lo, sh.least_hi, lo, hi);
         d.each(lo, hi, [&](int, float x) {
-            if (s.bin(x) <= (float)sh.least_hi && heavy(x))
+            const float b = s.bin(x);
+            if (b >= (float)least_lo && b <= (float)sh.least_hi && heavy(x))
                 atomicAdd(&sh.passed, 1u);
         });
         __syncthreads();

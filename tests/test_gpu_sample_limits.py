@@ -71,3 +71,24 @@ def test_borders_in_front_of_many_zeros(bd, rows, dtype):
     k = n - 2 * small + torch.linspace(1, small, rows).int()
     tokens, _ = bd.sample(l.to(DEV).expand(rows, n).contiguous(), torch.ones(rows, device=DEV), top_k=k.to(DEV))
     assert int((tokens.cpu().long() != order[k.long() - 1]).sum()) == 0
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("t,zero,below", [(3e38, 1e-10, 3e36), (1.0, 0.0, 0.03)])
+def test_min_p_below_logits_next_to_zero(bd, t, zero, below, rows):
+    """A border of min_p in the bin below zero, too full for a list, with zeros or logits that scale to nothing in front of it."""
+    g = torch.Generator().manual_seed(7)
+    n = 6000
+    l = torch.cat([-torch.rand(n, generator=g) * zero, -torch.rand(n, generator=g) * 0.99 * below - 0.01 * below, torch.full((n,), -3 * below)])
+    l = l[torch.randperm(len(l), generator=g)]
+    top, order = torch.sort(l.double(), descending=True, stable=True)
+    w = torch.exp((top - top[0]) / float(torch.tensor(t)))
+    for at in (n + 100, n + n // 2, 2 * n - 100):
+        # halfway between two neighbours or, as 32 bits hold it, a step away: no roundings of 64 bits decide
+        least = float(torch.sqrt(w[at - 1] * w[at]).float())
+        assert float((w - least).abs().min()) > 2.0 ** -45
+        kept = int((w >= least).sum())
+        tokens, logs = bd.sample(l.to(DEV).expand(rows, len(l)).contiguous(), torch.ones(rows, device=DEV), temperature=t, min_p=least)
+        assert int((tokens.cpu().long() != order[kept - 1]).sum()) == 0
+        want = torch.log(w[kept - 1] / w[:kept].sum())
+        assert ((logs.cpu().double() - want).abs() <= want.abs() * 2.0 ** -24 + 2.0 ** -35).all()
